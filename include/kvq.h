@@ -403,6 +403,155 @@ KVQ_API int kvq_h_decode_absorbed(const kvq_config *cfg, const kvq_layer *layer,
                                   int32_t out_dtype, void *scratch, uint64_t scratch_bytes,
                                   kvq_stream_t stream);
 
+/* ------------------------------------------------------------------ drafted tokens
+ * A step that verifies drafted tokens instead of decoding one: rotate and append the
+ * drafted rows (kvq_rope_append), attend with all of them at once under a tree mask
+ * (kvq_tree_attn), keep the accepted path's rows (kvq_tree_commit); kvq_read gives
+ * cached rows back as 16- or 32-bit values.  The source pages have no counterpart:
+ * they decode one token a step from keys that are already rotated.
+ * These calls keep the conventions above.  d_len / d_pos are device int32 [B]. */
+
+/* Rows of one tensor [B][n][heads][head_dim] inside a larger one (for example the
+ * query part of a fused projection's output): element strides between sequences and
+ * between tokens; the heads of a token are contiguous.  0 selects the contiguous
+ * stride (token: heads * head_dim; batch: n * token stride).  data is 16-byte aligned
+ * and both strides are multiples of 16 bytes, not negative. */
+typedef struct kvq_rows {
+    void *data;
+    int64_t batch_stride, token_stride;
+} kvq_rows;
+
+enum kvq_rope_layout {
+    KVQ_ROPE_HALF = 0,        /* element i pairs with i + rot_dim / 2               */
+    KVQ_ROPE_INTERLEAVED = 1  /* element 2i pairs with 2i + 1                       */
+};
+
+enum kvq_rope_scaling {
+    KVQ_ROPE_PLAIN = 0,   /* freq_i = base^(-2i / rot_dim)                          */
+    KVQ_ROPE_LINEAR = 1,  /* freq_i / factor                                        */
+    KVQ_ROPE_NTK = 2,     /* base grown to base * factor^(rot_dim / (rot_dim - 2))  */
+    KVQ_ROPE_YARN = 3,    /* freq_i / factor for pairs that turn less than `low` times
+                             in orig_len, freq_i for those that turn more than `high`
+                             times, a linear ramp over the pair index between (bounds
+                             rounded outwards to whole pairs); cos and sin times `gain` */
+    KVQ_ROPE_BANDS = 4    /* the same kept and stretched pairs with the ramp linear in
+                             the number of turns (low .. high)                      */
+};
+
+/* Rotary positions of a model.  The angle of pair i at position p is p * freq_i. */
+typedef struct kvq_rope_config {
+    int32_t rot_dim;   /* rotated elements at the start of each head: a multiple of 8,
+                          8 .. head_dim; the rest of the head passes through         */
+    int32_t layout;    /* KVQ_ROPE_HALF or KVQ_ROPE_INTERLEAVED                      */
+    int32_t scaling;   /* KVQ_ROPE_*                                                 */
+    int32_t orig_len;  /* YARN, BANDS: the length the frequencies were trained for   */
+    double base;       /* > 1                                                        */
+    double factor;     /* >= 1; ignored by PLAIN                                     */
+    double low, high;  /* YARN, BANDS: turns; 0 < low < high                         */
+    double gain;       /* factor on cos and sin; 0 selects 0.1 ln(factor) + 1 with
+                          YARN and 1 otherwise                                       */
+} kvq_rope_config;
+
+/* (cos, sin) of positions first_pos .. first_pos + n_pos - 1: table is device float
+ * [n_pos][rot_dim / 2][2].  Frequencies and angles are computed in 64 bits and only the
+ * results are rounded, so far positions are as exact as near ones.  A table is made once
+ * and serves every layer and step.  first_pos >= 0, first_pos + n_pos <= 2^31 - 1;
+ * n_pos 0 is a no-op.  Errors: INVALID_ARG, UNSUPPORTED (rot_dim), ALIGN, LAUNCH. */
+KVQ_API int kvq_rope_table(const kvq_rope_config *rope, int32_t first_pos, int32_t n_pos,
+                           float *table, kvq_stream_t stream);
+
+/* kvq_append with the rotation of the new queries and keys in the same launch (KV mode):
+ * token j < count_b of sequence b (count_b = d_count[b] clamped to [0, n_new], or n_new
+ * when d_count is NULL) is stored at position d_pos[b] + j and rotated by its rope
+ * position d_rope_pos[b * n_new + j] (d_rope_pos NULL: its storage position):
+ *   (a, b) -> (a cos - b sin, b cos + a sin) for each pair of the first rot_dim elements,
+ * in fp32 with every product and sum rounded once; rotated queries are then rounded to
+ * `dtype` (nearest even), rotated keys and the values are quantised from fp32 exactly as
+ * kvq_append quantises its input.
+ *   q, q_out  query rows in and out (n_q_heads heads), both NULL to rotate keys only;
+ *             q_out may be q's own rows (same data and strides), else they must not overlap
+ *   k, v      new key and value rows (n_kv_heads heads)
+ *   dtype     KVQ_F16, KVQ_F32 or KVQ_BF16, of all four
+ *   table, table_len  kvq_rope_table's output for positions 0 .. table_len - 1
+ *   max_pos_host  host bound of d_pos[], as kvq_append
+ * A token whose storage position is outside the cache (or whose page is invalid) is not
+ * stored, but its query is rotated; a token whose rope position is outside the table is
+ * skipped altogether.  Rows of tokens >= count_b are neither read nor written.
+ * With a sliding window a token that a later one of the same call overwrites is not stored.
+ * Errors: INVALID_ARG (h-mode included), UNSUPPORTED, CAPACITY (max_pos_host + n_new
+ * beyond the capacity, or beyond table_len with d_rope_pos NULL), ALIGN, LAUNCH. */
+KVQ_API int kvq_rope_append(const kvq_config *cfg, const kvq_layer *layer,
+                            const kvq_rope_config *rope, const float *table, int32_t table_len,
+                            const kvq_rows *q, const kvq_rows *k, const kvq_rows *v,
+                            const kvq_rows *q_out, int32_t dtype, const int32_t *d_pos,
+                            int32_t max_pos_host, int32_t n_new, const int32_t *d_count,
+                            const int32_t *d_rope_pos, kvq_stream_t stream);
+
+/* Read cached rows back: token j < count_b of sequence b (count_b as in kvq_rope_append,
+ * with n for n_new) is the cached token at position d_pos[b] + j; its value code * scale
+ * ((code - zero-point) * scale for KVQ_FMT_ASYM), exact in fp32, is rounded once to
+ * out_dtype (nearest even; F16 overflow gives an infinity).
+ *   k_out, v_out  output rows (n_kv_heads heads; h-mode: k_out is one row of d_model
+ *             elements per token and v_out is NULL); either may be NULL in KV mode
+ *   out_dtype KVQ_F16, KVQ_F32 or KVQ_BF16
+ *   max_pos_host  host bound of d_pos[]: CAPACITY if max_pos_host + n > capacity (not with
+ *             a sliding window, where a position's slot holds that token only while it is
+ *             an anchor or among the `window` most recent ones)
+ * Rows of tokens >= count_b, of positions outside the cache and of invalid pages are left
+ * as they were.  Errors: INVALID_ARG, UNSUPPORTED, CAPACITY, ALIGN, LAUNCH. */
+KVQ_API int kvq_read(const kvq_config *cfg, const kvq_layer *layer, const kvq_rows *k_out,
+                     const kvq_rows *v_out, int32_t out_dtype, const int32_t *d_pos,
+                     int32_t max_pos_host, int32_t n, const int32_t *d_count,
+                     kvq_stream_t stream);
+
+/* Most drafted tokens of one kvq_tree_attn / kvq_tree_commit call. */
+#define KVQ_TREE_MAX 64
+
+/* Attention of drafted tokens over a cache (KV mode, no sliding window).  Sequence b has
+ * L = d_len[b] cached tokens (clamped to [0, capacity]) and n = d_n_tree[b] drafted ones
+ * (clamped to [0, n_tree]; d_n_tree NULL: n_tree), stored at positions L .. L + n - 1
+ * (those beyond the capacity do not exist).  Query row i < n attends over every
+ * position < L and over drafted token j exactly when bit j of d_mask[b * n_tree + i] is set
+ * and j < n; d_mask NULL selects the causal mask j <= i (a chain).  For query head h of
+ * KV head h / G:
+ *   s_t = softmax_scale * q . k^_t,  p = softmax(s) over the attended t,  out = sum p_t v^_t
+ * with codes and scales exact, and fp32 scores, sums and accumulators; the probabilities
+ * enter the second product as p_t * (value scale) rounded to fp16 (relative error 2^-11 a
+ * token).  A row that attends nothing gets zeros; rows i >= n are left as they were.
+ * Masked places do not reach a row, whatever they hold; a row that attends a non-finite
+ * key or value gets an unspecified result.
+ *   q        device [B][n_tree][Hq][Dh], q_dtype KVQ_F16, KVQ_F32 or KVQ_BF16; G <= 8
+ *   n_tree   1 .. KVQ_TREE_MAX
+ *   max_len_host  host bound of d_len[]: max_len_host + n_tree <= capacity
+ *   d_mask   device uint64 [B][n_tree], 8-byte aligned, or NULL
+ *   out      device [B][n_tree][Hq][Dh], out_dtype KVQ_F16, KVQ_F32 or KVQ_BF16
+ *   workspace, num_ctas  as kvq_decode_attn, at least kvq_tree_workspace_bytes(cfg, n_tree,
+ *            num_ctas); its status word is read with kvq_workspace_status
+ * Errors: INVALID_ARG, UNSUPPORTED (window, G), CAPACITY, ALIGN, WORKSPACE, LAUNCH, DEVICE. */
+KVQ_API int kvq_tree_workspace_bytes(const kvq_config *cfg, int32_t n_tree, int32_t num_ctas,
+                                     uint64_t *bytes);
+KVQ_API int kvq_tree_attn(const kvq_config *cfg, const kvq_layer *layer, const void *q,
+                          int32_t q_dtype, int32_t n_tree, const int32_t *d_len,
+                          int32_t max_len_host, const int32_t *d_n_tree, const uint64_t *d_mask,
+                          float softmax_scale, void *out, int32_t out_dtype, void *workspace,
+                          uint64_t workspace_bytes, int32_t num_ctas, kvq_stream_t stream);
+
+/* Keep an accepted path (KV mode, no sliding window): for every sequence b, layer and KV
+ * head, the rows at positions L + path[i] move to L + i, i < m, L = d_len[b]; codes and
+ * scales are copied as they are.  path = d_path + b * path_stride holds drafted token
+ * indices in strictly ascending order below n_tree (a path from the root of a tree whose
+ * parents precede their children); m is d_n_path[b] clamped to [0, path_stride], cut before
+ * the first index that breaks this.  Other rows stay as they were.
+ *   layers   host array of n_layers layers of this config (one launch per 64)
+ *   d_len_out  device int32 [B] or NULL: receives L + m; not d_len itself
+ *   max_len_host  host bound of d_len[]: max_len_host + n_tree <= capacity
+ *   path_stride  1 .. n_tree;  n_tree  1 .. KVQ_TREE_MAX
+ * Errors: INVALID_ARG, UNSUPPORTED (window), CAPACITY, ALIGN, LAUNCH. */
+KVQ_API int kvq_tree_commit(const kvq_config *cfg, const kvq_layer *layers, int32_t n_layers,
+                            const int32_t *d_len, int32_t max_len_host, int32_t n_tree,
+                            const int32_t *d_path, int32_t path_stride, const int32_t *d_n_path,
+                            int32_t *d_len_out, kvq_stream_t stream);
+
 /* Read and clear the device status word a decode launch leaves in its
  * workspace: KVQ_OK, or KVQ_ERR_TIMEOUT if a kernel gave up a bounded wait
  * (its outputs are then invalid).  Synchronises `stream`. */

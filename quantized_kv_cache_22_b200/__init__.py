@@ -21,6 +21,9 @@ KVQ_OK = 0
 KVQ_MODE_KV, KVQ_MODE_H = 0, 1
 KVQ_FMT_INT, KVQ_FMT_E4M3, KVQ_FMT_ASYM, KVQ_FMT_TENSOR = 0, 1, 2, 3
 KVQ_F16, KVQ_F32, KVQ_BF16 = 0, 1, 2
+KVQ_ROPE_HALF, KVQ_ROPE_INTERLEAVED = 0, 1
+KVQ_ROPE_PLAIN, KVQ_ROPE_LINEAR, KVQ_ROPE_NTK, KVQ_ROPE_YARN, KVQ_ROPE_BANDS = 0, 1, 2, 3, 4
+KVQ_TREE_MAX = 64
 
 EXPORTED = ("kvq_cache_bytes", "kvq_layer_buffer_bytes", "kvq_append", "kvq_workspace_bytes",
             "kvq_h_scratch_bytes", "kvq_decode_attn", "kvq_decode_partials", "kvq_merge_partials",
@@ -29,7 +32,8 @@ EXPORTED = ("kvq_cache_bytes", "kvq_layer_buffer_bytes", "kvq_append", "kvq_work
             "kvq_append_decode_attn", "kvq_h_absorbed_scratch_bytes", "kvq_h_decode_absorbed",
             "kvq_h_fused_scratch_bytes", "kvq_h_decode_fused", "kvq_selftest_bounded_wait",
             "kvq_selftest_decode_timeout", "kvq_noalloc_status", "kvq_selftest_noalloc_timeout",
-            "kvq_decode_plan_info")
+            "kvq_decode_plan_info", "kvq_rope_table", "kvq_rope_append", "kvq_read",
+            "kvq_tree_workspace_bytes", "kvq_tree_attn", "kvq_tree_commit")
 
 
 class KvqError(RuntimeError):
@@ -59,6 +63,16 @@ class KvqLayer(ctypes.Structure):
     _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
                 ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
                 ("block_table", ctypes.c_void_p)]
+
+
+class KvqRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64)]
+
+
+class KvqRopeConfig(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("rot_dim", "layout", "scaling", "orig_len")] +
+                [(n, ctypes.c_double) for n in ("base", "factor", "low", "high", "gain")])
 
 
 def _load():
@@ -95,6 +109,17 @@ def _load():
         "kvq_selftest_noalloc_timeout": [cfgp, layp, P, i32, P, P, i32, u64, P],
         "kvq_decode_plan_info": [cfgp, i32, ctypes.POINTER(KvqDecodePlan)],
     }
+    rowp, ropep = ctypes.POINTER(KvqRows), ctypes.POINTER(KvqRopeConfig)
+    sig.update({
+        "kvq_rope_table": [ropep, i32, i32, P, P],
+        "kvq_rope_append": [cfgp, layp, ropep, P, i32, rowp, rowp, rowp, rowp, i32, P, i32, i32, P,
+                            P, P],
+        "kvq_read": [cfgp, layp, rowp, rowp, i32, P, i32, i32, P, P],
+        "kvq_tree_workspace_bytes": [cfgp, i32, i32, pu64],
+        "kvq_tree_attn": [cfgp, layp, P, i32, i32, P, i32, P, P, ctypes.c_float, P, i32, P, u64,
+                          i32, P],
+        "kvq_tree_commit": [cfgp, layp, i32, P, i32, i32, P, i32, P, P, P],
+    })
     for name, args in sig.items():
         f = getattr(lib, name)
         f.argtypes = args
@@ -247,6 +272,21 @@ class LayerCache:
         self.v_scales = alloc(max(vs // 2, 8), dtype=torch.float16, device=device) if vs else None
         self.cfg = cfg
         self.block_table = block_table
+
+    @classmethod
+    def from_buffers(cls, cfg: Config, k_codes, k_scales, v_codes, v_scales, block_table=None):
+        """A layer over buffers the caller already holds (contiguous; sized as
+        ``kvq_layer_buffer_bytes`` says; None for one the config does not use)."""
+        self = cls.__new__(cls)
+        parts = (k_codes, k_scales, v_codes, v_scales)
+        for t, need in zip(parts, kvq_layer_buffer_bytes(cfg)):
+            have = 0 if t is None else t.numel() * t.element_size()
+            if have < need or (t is not None and not t.is_contiguous()):
+                raise ValueError(f"a layer buffer is not contiguous or holds {have} of {need} bytes")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = parts
+        self.cfg = cfg
+        self.block_table = block_table
+        return self
 
     def c(self) -> KvqLayer:
         """A new ``kvq_layer`` struct with these buffers."""
@@ -436,3 +476,161 @@ def kvq_workspace_status(ws, stream=None) -> int:
     _check("kvq_workspace_status", _lib.kvq_workspace_status(_ptr(buf), ctypes.byref(st),
                                                              _stream(stream)))
     return st.value
+
+
+# ----------------------------------------------------------------------------- drafted tokens
+
+@dataclass
+class RopeConfig:
+    """Python view of ``kvq_rope_config`` (see include/kvq.h for the meaning of each field).
+    ``low`` and ``high`` default to 1 and 32 turns (YARN) or 1 and 4 (BANDS)."""
+    rot_dim: int
+    layout: int = KVQ_ROPE_HALF
+    scaling: int = KVQ_ROPE_PLAIN
+    base: float = 10000.0
+    factor: float = 1.0
+    orig_len: int = 0
+    low: float = 1.0
+    high: float = 0.0
+    gain: float = 0.0
+
+    def c(self) -> KvqRopeConfig:
+        high = self.high or (32.0 if self.scaling == KVQ_ROPE_YARN else 4.0)
+        return KvqRopeConfig(self.rot_dim, self.layout, self.scaling, self.orig_len, self.base,
+                             self.factor, self.low, high, self.gain)
+
+
+class TreeWorkspace(Workspace):
+    """Workspace of ``kvq_tree_attn`` (as Workspace: zero-filled, ready after every call)."""
+
+    def __init__(self, cfg: Config, n_tree: int, num_ctas: int = 0, device="cuda"):
+        v = ctypes.c_uint64()
+        _check("kvq_tree_workspace_bytes",
+               _lib.kvq_tree_workspace_bytes(cfg._ref(), int(n_tree), int(num_ctas), ctypes.byref(v)))
+        self.nbytes = v.value
+        self.n_tree = n_tree
+        self.buf = torch.zeros(self.nbytes // 4 + 64, dtype=torch.float32, device=device)
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _here(*tensors):
+    """The kernels run on the current device: every tensor has to be there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+
+
+def _ints(t, shape, what: str):
+    if t is not None and (t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous()):
+        raise ValueError(f"{what} is a contiguous int32 tensor of shape {tuple(shape)}")
+
+
+def _rows(t: torch.Tensor, n: int, heads: int, dim: int, batch: int, dtype, what: str):
+    """byref() of the kvq_rows of a [B][n][heads][dim] view (or None)."""
+    if t is None:
+        return None
+    if t.shape != (batch, n, heads, dim) or t.dtype != dtype:
+        raise ValueError(f"{what} is {dtype} of shape {(batch, n, heads, dim)}")
+    sb, st, sh, sd = t.stride()
+    if t.numel() and ((sd != 1 and dim > 1) or (sh != dim and heads > 1)):
+        raise ValueError(f"the heads of a token of {what} are contiguous")
+    if (sb == 0 and batch > 1) or (st == 0 and n > 1):
+        raise ValueError(f"{what} is an expanded view: its rows share memory")
+    # a stride that no index uses is whatever torch says: 0 selects the contiguous one
+    return ctypes.byref(KvqRows(t.data_ptr(), sb if batch > 1 else 0, st if n > 1 else 0))
+
+
+def kvq_rope_table(rope: RopeConfig, n_pos: int, first_pos: int = 0, table=None, device="cuda",
+                   stream=None) -> torch.Tensor:
+    """(cos, sin) of positions first_pos ..: float32 [n_pos][rot_dim/2][2], made once per model."""
+    if table is None:
+        table = torch.empty(n_pos, rope.rot_dim // 2, 2, dtype=torch.float32, device=device)
+    _need(table.dtype == torch.float32 and table.is_contiguous() and
+          table.shape == (n_pos, rope.rot_dim // 2, 2), "table is contiguous float32 [n_pos][rot_dim/2][2]")
+    _here(table)
+    _check("kvq_rope_table", _lib.kvq_rope_table(ctypes.byref(rope.c()), int(first_pos), int(n_pos),
+                                                 _ptr(table), _stream(stream)))
+    return table
+
+
+def kvq_rope_append(cfg: Config, layer: LayerCache, rope: RopeConfig, table: torch.Tensor, q, k: torch.Tensor,
+                    v: torch.Tensor, q_out, d_pos: torch.Tensor, max_pos: int, d_count=None, d_rope_pos=None,
+                    stream=None):
+    """Rotate new queries and keys and quantise keys and values into the cache, in one launch.
+    q, q_out [B][n][Hq][Dh] (both None: keys only), k, v [B][n][Hkv][Dh]: views whose token and
+    batch strides are free (e.g. parts of one projection's output)."""
+    B, n = k.shape[:2]
+    _need(table.dtype == torch.float32 and table.is_contiguous() and table.dim() == 3 and
+          table.shape[1:] == (rope.rot_dim // 2, 2), "table is contiguous float32 [positions][rot_dim/2][2]")
+    _here(layer.k_codes, table, q, k, v, q_out, d_pos, d_count, d_rope_pos)
+    _ints(d_pos, (cfg.batch,), "d_pos")
+    _ints(d_count, (cfg.batch,), "d_count")
+    _ints(d_rope_pos, (cfg.batch, n), "d_rope_pos")
+    _check("kvq_rope_append", _lib.kvq_rope_append(
+        cfg._ref(), layer._ref(), ctypes.byref(rope.c()), _ptr(table), table.shape[0],
+        _rows(q, n, cfg.n_q_heads, cfg.head_dim, cfg.batch, k.dtype, "q"),
+        _rows(k, n, cfg.n_kv_heads, cfg.head_dim, cfg.batch, k.dtype, "k"),
+        _rows(v, n, cfg.n_kv_heads, cfg.head_dim, cfg.batch, k.dtype, "v"),
+        _rows(q_out, n, cfg.n_q_heads, cfg.head_dim, cfg.batch, k.dtype, "q_out"),
+        _dtype_code(k), _ptr(d_pos), int(max_pos), n, _ptr(d_count), _ptr(d_rope_pos), _stream(stream)))
+
+
+def kvq_read(cfg: Config, layer: LayerCache, k_out, v_out, d_pos: torch.Tensor, max_pos: int, d_count=None,
+             stream=None):
+    """Cached tokens d_pos .. d_pos + n - 1 as values: k_out, v_out [B][n][Hkv][Dh] (either None;
+    h-mode: k_out [B][n][d_model]), views as in kvq_rope_append."""
+    some = k_out if k_out is not None else v_out
+    _need(some is not None, "k_out or v_out is given")
+    n = some.shape[1]
+    _here(layer.k_codes, k_out, v_out, d_pos, d_count)
+    _ints(d_pos, (cfg.batch,), "d_pos")
+    _ints(d_count, (cfg.batch,), "d_count")
+    heads, dim = cfg.n_kv_heads, cfg.head_dim
+    if cfg.mode == KVQ_MODE_H:
+        heads, dim = 1, cfg.d_model
+        k_out = None if k_out is None else k_out.unsqueeze(2)
+    _check("kvq_read", _lib.kvq_read(
+        cfg._ref(), layer._ref(), _rows(k_out, n, heads, dim, cfg.batch, some.dtype, "k_out"),
+        _rows(v_out, n, heads, dim, cfg.batch, some.dtype, "v_out"), _dtype_code(some), _ptr(d_pos),
+        int(max_pos), n, _ptr(d_count), _stream(stream)))
+
+
+def kvq_tree_attn(cfg: Config, layer: LayerCache, q: torch.Tensor, d_len: torch.Tensor, max_len: int, d_mask,
+                  out: torch.Tensor, ws: TreeWorkspace, d_n_tree=None, softmax_scale: float = 0.0,
+                  num_ctas: int = 0, stream=None):
+    """Attention of drafted tokens: q, out [B][n_tree][Hq][Dh], d_len cached tokens before them,
+    d_mask int64 [B][n_tree] (bit j: the token attends drafted token j; None: causal)."""
+    shape = (cfg.batch, q.shape[1], cfg.n_q_heads, cfg.head_dim)
+    _need(q.shape == shape and out.shape == shape and q.is_contiguous() and out.is_contiguous(),
+          "q and out are contiguous [B][n_tree][Hq][Dh]")
+    if d_mask is not None:
+        _need(d_mask.dtype == torch.int64 and d_mask.shape == shape[:2] and d_mask.is_contiguous(),
+              "d_mask is a contiguous int64 tensor [B][n_tree]")
+    _here(layer.k_codes, q, d_len, d_mask, d_n_tree, out, ws.buf)
+    _ints(d_len, (cfg.batch,), "d_len")
+    _ints(d_n_tree, (cfg.batch,), "d_n_tree")
+    _check("kvq_tree_attn", _lib.kvq_tree_attn(
+        cfg._ref(), layer._ref(), _ptr(q), _dtype_code(q), shape[1], _ptr(d_len), int(max_len), _ptr(d_n_tree),
+        _ptr(d_mask), float(softmax_scale), _ptr(out), _dtype_code(out), _ptr(ws.buf), ws.nbytes, int(num_ctas),
+        _stream(stream)))
+
+
+def kvq_tree_commit(cfg: Config, layers, d_len: torch.Tensor, max_len: int, d_path: torch.Tensor,
+                    d_n_path: torch.Tensor, n_tree: int, d_len_out=None, stream=None):
+    """Keep the accepted path of every sequence in all `layers` (LayerCache objects) at once:
+    row d_len + path[i] moves to d_len + i; d_len_out receives d_len + the path's length."""
+    _need(d_path.dim() == 2, "d_path is a contiguous int32 tensor [B][n]")
+    _here(d_len, d_path, d_n_path, d_len_out, *(x.k_codes for x in layers))
+    _ints(d_len, (cfg.batch,), "d_len")
+    _ints(d_path, (cfg.batch, d_path.shape[1]), "d_path")
+    _ints(d_n_path, (cfg.batch,), "d_n_path")
+    _ints(d_len_out, (cfg.batch,), "d_len_out")
+    arr = (KvqLayer * len(layers))(*(x.c() for x in layers))
+    _check("kvq_tree_commit", _lib.kvq_tree_commit(
+        cfg._ref(), arr, len(layers), _ptr(d_len), int(max_len), int(n_tree), _ptr(d_path), d_path.shape[1],
+        _ptr(d_n_path), _ptr(d_len_out), _stream(stream)))

@@ -17,9 +17,11 @@ using namespace kvq;
 
 namespace {
 
-constexpr uint64_t kTimeoutNs = 1000000000ull;  // bounded waits give up after ~1 s
-
 thread_local char g_detail[160] = "";
+
+}  // namespace
+
+namespace kvq {
 
 // Record which step failed with which CUDA error (read by kvq_last_error_detail).
 int fail(const char *where, cudaError_t e)
@@ -90,6 +92,23 @@ int scale_row_vals(const kvq_config *c, int bits, int group)
     if (bits == 16 || c->kv_format == KVQ_FMT_TENSOR) return 0;
     return scale_groups(c->head_dim, bits, group) * scale_vals(c->kv_format);
 }
+
+int check_kv_layer(const kvq_config *cfg, const kvq_layer *layer)
+{
+    if (!layer->k_codes || !layer->v_codes) return KVQ_ERR_INVALID_ARG;
+    if (cfg->page_tokens && !layer->block_table) return KVQ_ERR_INVALID_ARG;
+    if ((cfg->k_bits != 16 && !layer->k_scales) || (cfg->v_bits != 16 && !layer->v_scales))
+        return KVQ_ERR_INVALID_ARG;
+    if (!aligned16(layer->k_codes) || !aligned16(layer->v_codes) ||
+        (layer->k_scales && !aligned16(layer->k_scales)) ||
+        (layer->v_scales && !aligned16(layer->v_scales)))
+        return KVQ_ERR_ALIGN;
+    return KVQ_OK;
+}
+
+}  // namespace kvq
+
+namespace {
 
 // ---------------------------------------------------------------- TMA encode
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -179,7 +198,9 @@ bool encode_codes_map_uncached(CUtensorMap *m, const void *codes, int bh, int ca
     return r == CUDA_SUCCESS;
 }
 
-int current_device_props(int *sms, int *max_smem)
+}  // namespace
+
+int kvq::current_device_props(int *sms, int *max_smem)
 {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return KVQ_ERR_DEVICE;
@@ -214,6 +235,8 @@ int current_device_props(int *sms, int *max_smem)
     }
     return KVQ_OK;
 }
+
+namespace {
 
 // Shapes of the attention half (KV mode, or h-mode after reconstruction).
 struct AttnShape {
@@ -582,19 +605,6 @@ static int decode_kv_layout(const kvq_config *cfg, const void *k_codes, const vo
         cudaError_t e = launch_merge(mp, stream);
         if (e != cudaSuccess) return fail("merge launch", e);
     }
-    return KVQ_OK;
-}
-
-static int check_kv_layer(const kvq_config *cfg, const kvq_layer *layer)
-{
-    if (!layer->k_codes || !layer->v_codes) return KVQ_ERR_INVALID_ARG;
-    if (cfg->page_tokens && !layer->block_table) return KVQ_ERR_INVALID_ARG;
-    if ((cfg->k_bits != 16 && !layer->k_scales) || (cfg->v_bits != 16 && !layer->v_scales))
-        return KVQ_ERR_INVALID_ARG;
-    if (!aligned16(layer->k_codes) || !aligned16(layer->v_codes) ||
-        (layer->k_scales && !aligned16(layer->k_scales)) ||
-        (layer->v_scales && !aligned16(layer->v_scales)))
-        return KVQ_ERR_ALIGN;
     return KVQ_OK;
 }
 

@@ -10,6 +10,15 @@
 
 namespace kvq {
 
+// ------------------------------------------------------------------ host checks (kvq_api.cu)
+constexpr uint64_t kTimeoutNs = 1000000000ull;  // bounded waits give up after ~1 s
+int fail(const char *where, cudaError_t e);     // records the step for kvq_last_error_detail
+bool aligned16(const void *p);
+int check_cfg(const kvq_config *c);
+int check_kv_layer(const kvq_config *cfg, const kvq_layer *layer);
+int scale_row_vals(const kvq_config *c, int bits, int group);   // fp16 values per row's scales
+int current_device_props(int *sms, int *max_smem);
+
 // ------------------------------------------------------------------ append
 struct AppendParams {
     const void *x;          // [B][n_new][rows_per_tok][dim] input
@@ -38,6 +47,97 @@ __host__ __device__ inline int cache_slot(int t, int window, int n_anchor)
 
 cudaError_t launch_append(const AppendParams &k, const AppendParams *v, cudaStream_t stream);
 
+// ------------------------------------------------------------------ drafted tokens
+// Where a layer's rows lie: contiguous, ring or paged (pages of kPageTokens rows).
+struct CacheRows {
+    int32_t batch, heads, cap;        // heads: rows per token
+    int32_t window, n_anchor;
+    const int32_t *block_table;       // paged: [batch][max_pages]
+    int32_t max_pages, n_pages;
+};
+
+// Row (of one head's codes or scales) that holds position pos of sequence b, or -1 when
+// the position is outside the cache or its page is not a pool page.
+__device__ __forceinline__ int64_t cache_row(const CacheRows &c, int b, int head, int64_t pos)
+{
+    if (pos < 0 || pos > 0x7fffffff) return -1;
+    const int slot = cache_slot((int)pos, c.window, c.n_anchor);
+    if (slot >= c.cap) return -1;
+    if (c.block_table == nullptr) return ((int64_t)b * c.heads + head) * c.cap + slot;
+    const int page = c.block_table[(int64_t)b * c.max_pages + slot / kPageTokens];
+    if (page < 0 || page >= c.n_pages) return -1;
+    return ((int64_t)page * c.heads + head) * kPageTokens + slot % kPageTokens;
+}
+
+// One of K and V in a layer
+struct CacheTensor {
+    uint8_t *codes;
+    __half *scales;
+    int32_t bits, group;              // group: elements per scale (32 at 16 bits)
+};
+
+struct RowsView {                     // kvq_rows with its strides resolved
+    void *data;
+    int64_t batch_stride, token_stride;
+};
+
+struct RopeAppendParams {
+    CacheRows rows;
+    CacheTensor k, v;
+    RowsView q_in, q_out, k_in, v_in; // q_in.data null: no queries
+    const float2 *table;              // [table_len][rot / 2]
+    const int32_t *d_pos, *d_count, *d_rope_pos;
+    int32_t table_len, rot, interleaved, dtype, fmt;
+    int32_t n_new, n_q_heads, dh;
+};
+cudaError_t launch_rope_append(const RopeAppendParams &p, cudaStream_t stream);
+
+struct RopeTableParams {
+    double freq[64];
+    double gain;
+    float2 *table;
+    int32_t first_pos, n_pos, pairs;
+};
+cudaError_t launch_rope_table(const RopeTableParams &p, cudaStream_t stream);
+
+struct ReadParams {
+    CacheRows rows;
+    CacheTensor t[2];
+    RowsView out[2];                  // data null: not wanted
+    const int32_t *d_pos, *d_count;
+    int32_t n, dim, fmt, out_dtype;   // dim: elements of one row
+};
+cudaError_t launch_read(const ReadParams &p, cudaStream_t stream);
+
+constexpr int kCommitLayers = 64;     // layers of one commit launch
+struct CommitParams {
+    CacheRows rows;                   // block_table unused: see table
+    const int32_t *table[kCommitLayers];
+    uint8_t *codes[2][kCommitLayers];
+    __half *scales[2][kCommitLayers];
+    int32_t row_bytes[2], scale_bytes[2];
+    int32_t n_layers, n_tree, path_stride;
+    const int32_t *d_len, *d_path, *d_n_path;
+    int32_t *d_len_out;
+};
+cudaError_t launch_commit(const CommitParams &p, cudaStream_t stream);
+
+struct TreeParams {
+    CacheRows rows;
+    CacheTensor k, v;
+    const void *q;
+    void *out;
+    const int32_t *d_len, *d_n_tree;
+    const uint64_t *d_mask;
+    int32_t q_dtype, out_dtype, fmt;
+    int32_t n_tree, n_q_heads, G, dh;
+    float tau_log2e;
+};
+cudaError_t launch_tree(const TreeParams &p, cudaStream_t stream);
+
+// A workspace starts with a status word and padding.
+constexpr int kWorkspaceHeaderFloats = 64;
+
 // ------------------------------------------------------------------ decode
 constexpr int kDecodeConsumerWarps = 4;
 constexpr int kDecodeTileTokens = 32 * kDecodeConsumerWarps;   // tokens per stage (32 per warp)
@@ -46,7 +146,6 @@ constexpr int kDecodeThreads = 32 * (kDecodeConsumerWarps + 2);
 // CTAs per SM the decode kernel is compiled for (168 registers per thread) and its
 // shared-memory ring is planned for
 constexpr int kDecodeCtasPerSm = 2;
-constexpr int kWorkspaceHeaderFloats = 64;                      // status word + padding
 // The new token's K/V for the append step fused into the decode kernel.
 struct FusedAppend {
     const void *k_new, *v_new;    // [B][Hkv][Dh] in dtype; null: no append
