@@ -99,6 +99,24 @@ void rope_frequencies(const kvq_rope_config *r, double *freq, double *gain)
     *gain = r->gain != 0.0 ? r->gain : (r->scaling == KVQ_ROPE_YARN ? 0.1 * std::log(r->factor) + 1.0 : 1.0);
 }
 
+// CTAs of a tree launch: one per SM unless the caller says otherwise.
+int tree_ctas(int32_t num_ctas, int32_t *ctas)
+{
+    int sms = 0, smem = 0;
+    if (num_ctas == 0) {
+        const int rc = current_device_props(&sms, &smem);
+        if (rc) return rc;
+    }
+    *ctas = num_ctas ? num_ctas : sms;
+    return KVQ_OK;
+}
+
+uint64_t tree_seg_bytes(const kvq_config *cfg, int32_t n_tree, int G)
+{
+    const uint64_t n = (uint64_t)cfg->batch * cfg->n_kv_heads * tree_row_tiles(n_tree, G) * sizeof(int4);
+    return (n + 255) / 256 * 256;
+}
+
 // What every KV-mode call here needs of its configuration and layer.
 int check_draft(const kvq_config *cfg, const kvq_layer *layer)
 {
@@ -219,7 +237,11 @@ int kvq_tree_workspace_bytes(const kvq_config *cfg, int32_t n_tree, int32_t num_
     if (cfg->mode != KVQ_MODE_KV || !bytes || num_ctas < 0 || n_tree < 1 || n_tree > KVQ_TREE_MAX)
         return KVQ_ERR_INVALID_ARG;
     if (cfg->window != 0 || cfg->n_q_heads / cfg->n_kv_heads > 8) return KVQ_ERR_UNSUPPORTED;
-    *bytes = (uint64_t)kWorkspaceHeaderFloats * 4;
+    rc = tree_ctas(num_ctas, &num_ctas);
+    if (rc) return rc;
+    const int G = cfg->n_q_heads / cfg->n_kv_heads;
+    *bytes = (uint64_t)kWorkspaceHeaderFloats * 4 + tree_seg_bytes(cfg, n_tree, G) +
+             2ull * num_ctas * tree_slot_floats(tree_slot_rows(n_tree, G), cfg->head_dim) * 4;
     return KVQ_OK;
 }
 
@@ -258,6 +280,19 @@ int kvq_tree_attn(const kvq_config *cfg, const kvq_layer *layer, const void *q, 
     p.dh = cfg->head_dim;
     const float scale = softmax_scale != 0.f ? softmax_scale : 1.f / std::sqrt((float)cfg->head_dim);
     p.tau_log2e = scale * 1.4426950408889634f;
+    p.timeout_ns = kTimeoutNs;
+    p.row_tiles = tree_row_tiles(n_tree, p.G);
+    p.slot_rows = tree_slot_rows(n_tree, p.G);
+    p.status = static_cast<int *>(workspace);
+    uint8_t *ws = static_cast<uint8_t *>(workspace) + kWorkspaceHeaderFloats * 4;
+    p.seg = reinterpret_cast<int4 *>(ws);
+    p.slots = reinterpret_cast<float *>(ws + tree_seg_bytes(cfg, n_tree, p.G));
+    int sms = 0, max_smem = 0;
+    rc = current_device_props(&sms, &max_smem);
+    if (rc) return rc;
+    if (!plan_tree(p, max_smem, &p.l)) return KVQ_ERR_UNSUPPORTED;
+    rc = tree_ctas(num_ctas, &p.l.num_ctas);
+    if (rc) return rc;
     cudaError_t e = launch_tree(p, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? KVQ_OK : fail("tree attention launch", e);
 }

@@ -74,6 +74,30 @@ struct Codes8<16> {
     }
 };
 
+// Four values at element idx (a multiple of 4), or two (a multiple of 2).
+__device__ __forceinline__ void store4(void *base, int64_t idx, int dtype, const float (&x)[4])
+{
+    if (dtype == KVQ_F32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(base) + idx) = make_float4(x[0], x[1], x[2], x[3]);
+    } else if (dtype == KVQ_F16) {
+        __half2 h[2] = {__floats2half2_rn(x[0], x[1]), __floats2half2_rn(x[2], x[3])};
+        *reinterpret_cast<uint2 *>(static_cast<__half *>(base) + idx) = *reinterpret_cast<uint2 *>(h);
+    } else {
+        __nv_bfloat162 h[2] = {__floats2bfloat162_rn(x[0], x[1]), __floats2bfloat162_rn(x[2], x[3])};
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(base) + idx) = *reinterpret_cast<uint2 *>(h);
+    }
+}
+
+__device__ __forceinline__ void store2(void *base, int64_t idx, int dtype, const float (&x)[2])
+{
+    if (dtype == KVQ_F32)
+        *reinterpret_cast<float2 *>(static_cast<float *>(base) + idx) = make_float2(x[0], x[1]);
+    else if (dtype == KVQ_F16)
+        *reinterpret_cast<__half2 *>(static_cast<__half *>(base) + idx) = __floats2half2_rn(x[0], x[1]);
+    else
+        *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(base) + idx) = __floats2bfloat162_rn(x[0], x[1]);
+}
+
 // Eight values at element idx (a multiple of 8) of an array of dtype.
 __device__ __forceinline__ void store8(void *base, int64_t idx, int dtype, const float (&x)[8])
 {

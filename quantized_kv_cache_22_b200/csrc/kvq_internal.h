@@ -122,6 +122,17 @@ struct CommitParams {
 };
 cudaError_t launch_commit(const CommitParams &p, cudaStream_t stream);
 
+// How a converted tile's codes become f16 operands: the code kinds, and whether the scales of
+// a row's groups go into the operand (as two f16 parts) or stay outside it (one per row).
+struct TreeLaunch {
+    int32_t num_ctas, entries;        // raw tiles of K or V in the ring
+    uint32_t entry_bytes, off_scales; // bytes of a ring entry, and its scales inside
+    uint32_t off_k, off_v;            // converted tiles (k_bufs, v_bufs of them)
+    uint32_t k_bytes, v_bytes, lo;    // bytes of one, and of its first f16 part
+    int32_t k_bufs, v_bufs, k_grouped, v_grouped;
+    uint32_t off_stage, off_par, off_ctl;
+    size_t smem_bytes;
+};
 struct TreeParams {
     CacheRows rows;
     CacheTensor k, v;
@@ -129,10 +140,22 @@ struct TreeParams {
     void *out;
     const int32_t *d_len, *d_n_tree;
     const uint64_t *d_mask;
+    int *status;
+    int4 *seg;                        // [B][Hkv][row tiles]: first slot, first CTA, CTAs
+    float *slots;                     // partials: [2 * num_ctas] of slot_floats
     int32_t q_dtype, out_dtype, fmt;
     int32_t n_tree, n_q_heads, G, dh;
+    int32_t row_tiles, slot_rows;     // tiles of kTreeRows query rows of a KV head, rows of a slot
     float tau_log2e;
+    uint64_t timeout_ns;
+    TreeLaunch l;
 };
+constexpr int kTreeRows = 128;
+inline int tree_row_tiles(int n_tree, int G) { return (n_tree * G + kTreeRows - 1) / kTreeRows; }
+inline int tree_slot_rows(int n_tree, int G) { return n_tree * G < kTreeRows ? n_tree * G : kTreeRows; }
+__host__ __device__ constexpr int64_t tree_slot_floats(int rows, int dh) { return (int64_t)rows * (dh + 2); }
+// Fill in the launch (but num_ctas) for this device's shared memory.
+bool plan_tree(const TreeParams &p, int max_smem, TreeLaunch *l);
 cudaError_t launch_tree(const TreeParams &p, cudaStream_t stream);
 
 // A workspace starts with a status word and padding.

@@ -3,6 +3,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "kvq_dequant.cuh"
 #include "kvq_internal.h"
 #include "kvq_quant.cuh"
 
@@ -20,19 +21,6 @@ __global__ void __launch_bounds__(256) rope_table_kernel(const __grid_constant__
     double s, c;
     sincos(angle, &s, &c);
     p.table[i] = make_float2((float)(c * p.gain), (float)(s * p.gain));
-}
-
-__device__ __forceinline__ void store4(void *base, int64_t idx, int dtype, const float (&x)[4])
-{
-    if (dtype == KVQ_F32) {
-        *reinterpret_cast<float4 *>(static_cast<float *>(base) + idx) = make_float4(x[0], x[1], x[2], x[3]);
-    } else if (dtype == KVQ_F16) {
-        __half2 h[2] = {__floats2half2_rn(x[0], x[1]), __floats2half2_rn(x[2], x[3])};
-        *reinterpret_cast<uint2 *>(static_cast<__half *>(base) + idx) = *reinterpret_cast<uint2 *>(h);
-    } else {
-        __nv_bfloat162 h[2] = {__floats2bfloat162_rn(x[0], x[1]), __floats2bfloat162_rn(x[2], x[3])};
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(base) + idx) = *reinterpret_cast<uint2 *>(h);
-    }
 }
 
 // A row is DH/4 lanes of four elements, so a warp handles 128/DH rows at a time and every
