@@ -53,7 +53,7 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr uint32_t COL_S = 0, COL_O = 256, COL_Q = 384, COL_QLO = 448;   // TMEM columns
 constexpr uint32_t PANEL = TT * 128;    // 64 f16 of every token
 
-// P in [0, 2^14]: m starts 2^6 below the first tile's maximum and follows it when 2^14 is passed
+// P in [0, 2^14]: m starts 6 to 7 below the first chunk's maximum and follows when 14 is passed
 constexpr float kHead = 6.f, kMoveAt = 14.f;
 
 struct Work {
@@ -274,13 +274,16 @@ __device__ __forceinline__ void convert(const uint8_t *raw, const uint16_t *sc, 
                                         int nvalid, int ct, int ng, int gshift, float tensor, bool is_tensor,
                                         float *p0, float *p1)
 {
-    constexpr int CH = DH / 8, RPP = kConvThreads / CH, PASSES = TT / RPP, BATCH = 4;
-    constexpr int ROW = CH * Raw<KIND>::BYTES;
+    // A thread's pieces are eight codes wide: eight lanes a 64-element panel row (one
+    // 128-byte operand row, so that their 16-byte stores hit all banks), four tokens a warp,
+    // both panels of a 128-element row.  Neighbouring tokens take the panels in turns, so that
+    // the lanes' loads hit all banks too.
+    constexpr int ROW = DH / 8 * Raw<KIND>::BYTES, PANELS = DH / 64, RPP = kConvThreads / 8, PASSES = TT / RPP;
     constexpr int PAIR = KIND == K_ASYM ? 2 : 1;
     // elements that are not numbers: dropped, and the token's queries told by log2 = NaN
     constexpr bool CHECK = ISV && (KIND == K_E4M3 || KIND == K_F16);
-    const int c = ct % CH, tr = ct / CH, lane = ct & 31;
-    const int g = (c * 8) >> gshift;
+    const int c = ct & 7, tr = ct >> 3, lane = ct & 31;
+    const int turn = KIND == K_INT4 ? (tr >> 1) & 1 : tr & 1;
 
     auto params = [&](int t, bool bad) {
         if constexpr (GRP) {
@@ -310,22 +313,26 @@ __device__ __forceinline__ void convert(const uint8_t *raw, const uint16_t *sc, 
     };
     if (!CHECK && ct < TT) params(ct, false);
 
+    const uint8_t *src = raw + tr * ROW + c * Raw<KIND>::BYTES;
+    uint8_t *out = dst + tr * 128 + ((c ^ tr) & 7) * 16;      // (t ^ tr) & 7 = 0: RPP is a multiple of 8
+    uint32_t bad_rows = 0;                                     // CHECK: bit u for pass u
+    // (kept a loop: the roles' code together has to stay within the instruction cache)
+#pragma unroll 1
+    for (int pn = 0; pn < PANELS; pn++) {
+        const int panel = PANELS == 2 ? pn ^ turn : 0;
+        const int g = (c * 8 + 64 * panel) >> gshift;
+        Raw<KIND> r[PASSES];
 #pragma unroll
-    for (int pb = 0; pb < PASSES; pb += BATCH) {
-        Raw<KIND> r[BATCH];
+        for (int u = 0; u < PASSES; u++)
+            r[u].w = *reinterpret_cast<const decltype(r[u].w) *>(src + u * RPP * ROW + panel * 8 * Raw<KIND>::BYTES);
 #pragma unroll
-        for (int u = 0; u < BATCH; u++)
-            r[u].w = *reinterpret_cast<const decltype(r[u].w) *>(raw + ((pb + u) * RPP + tr) * ROW +
-                                                               c * Raw<KIND>::BYTES);
-#pragma unroll
-        for (int u = 0; u < BATCH; u++) {
-            const int t = (pb + u) * RPP + tr;
-            uint32_t h[4], l[4] = {0u, 0u, 0u, 0u};
-            uint32_t zero = 0u;
-            bool drop = ISV && t >= nvalid;
+        for (int u = 0; u < PASSES; u++) {
+            const int t = u * RPP + tr;
+            uint32_t h[4], zero = 0u;
             if constexpr (KIND == K_ASYM) {
                 const uint32_t z = sc[(t * ng + g) * PAIR + 1];
-                zero = hadd2_u32(z * 0x10001u, 0x64006400u);
+                // a zero-point that is no number must not reach the rows that mask the token
+                zero = hadd2_u32((ISV && z > 0x5bf8u ? 0u : z) * 0x10001u, 0x64006400u);
             }
             codes_f16<KIND>(r[u], zero, h);
             if constexpr (CHECK) {
@@ -336,31 +343,40 @@ __device__ __forceinline__ void convert(const uint8_t *raw, const uint16_t *sc, 
                     any |= inf;
                     h[k] &= ~((inf >> 15) * 0xFFFFu);
                 }
-                const unsigned votes = __ballot_sync(FULL, any != 0 && t < nvalid);
-                const unsigned mine = (votes >> (lane / CH * CH)) & ((1u << CH) - 1u);
-                if (c == 0) params(t, mine != 0);
+                const unsigned votes = __ballot_sync(FULL, any != 0);
+                if ((votes >> (lane & 24)) & 0xFFu) bad_rows |= 1u << u;
             }
+            uint8_t *d = out + u * RPP * 128 + panel * PANEL;
             if constexpr (GRP) {
                 const RowScale rs = row_scale<KIND>(sc, t, ng);
-                drop |= ISV && rs.bad;
-                const float s = __half2float(__ushort_as_half(sc[(t * ng + g) * PAIR])) * pow2i(-rs.e);
+                float s = __half2float(__ushort_as_half(sc[(t * ng + g) * PAIR])) * pow2i(-rs.e);
+                if (ISV && rs.bad) s = 0.f;
                 const uint32_t s2 = pack_half2(s, s);
+                uint32_t l[4];
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
                     const uint32_t hi = hmul2_u32(h[k], s2);
                     l[k] = hfma2_u32(h[k], s2, hi ^ 0x80008000u);
                     h[k] = hi;
                 }
-            } else if constexpr (KIND == K_ASYM && ISV) {
-                drop |= (sc[t * PAIR + 1] & 0x7fff) > 0x5bf8;
+                *reinterpret_cast<uint4 *>(d + lo_off) = make_uint4(l[0], l[1], l[2], l[3]);
             }
-            if (drop) {
-                h[0] = h[1] = h[2] = h[3] = 0u;
-                l[0] = l[1] = l[2] = l[3] = 0u;
-            }
-            uint8_t *d = dst + (uint32_t)(c >> 3) * PANEL + (uint32_t)t * 128u + (uint32_t)(((c ^ t) & 7) << 4);
             *reinterpret_cast<uint4 *>(d) = make_uint4(h[0], h[1], h[2], h[3]);
-            if constexpr (GRP) *reinterpret_cast<uint4 *>(d + lo_off) = make_uint4(l[0], l[1], l[2], l[3]);
+        }
+    }
+    if (CHECK && c == 0)
+#pragma unroll 1
+        for (int u = 0; u < PASSES; u++) params(u * RPP + tr, (bad_rows >> u) & 1u);
+    if (ISV && nvalid < TT) {
+        // the last tile: zeros past the sequence's end
+        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+        for (int u = 0; u < PASSES; u++) {
+            if (u * RPP + tr < nvalid) continue;
+            for (int pn = 0; pn < PANELS; pn++) {
+                *reinterpret_cast<uint4 *>(out + u * RPP * 128 + pn * PANEL) = none;
+                if (GRP) *reinterpret_cast<uint4 *>(out + u * RPP * 128 + pn * PANEL + lo_off) = none;
+            }
         }
     }
 }
@@ -401,51 +417,74 @@ __device__ __forceinline__ uint32_t visible(int tok, int len, uint64_t mask)
     return d < 64 ? (uint32_t)(mask >> d) : 0u;
 }
 
-// z of 32 tokens: scores (fp32 accumulators in r) times the row's and the tokens' factors
-__device__ __forceinline__ void scores32(const uint32_t (&r)[32], const float *sk, const float *lv, float rf,
-                                         uint32_t vis, float *z)
+// Two fp32 numbers in a register pair, and the packed instructions on them.
+__device__ __forceinline__ uint64_t pair(uint32_t a, uint32_t b) { return (uint64_t)b << 32 | a; }
+__device__ __forceinline__ uint64_t pair(float a, float b) { return pair(__float_as_uint(a), __float_as_uint(b)); }
+__device__ __forceinline__ float first(uint64_t x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float second(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
 {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// z of 32 tokens (scores, fp32 accumulators in a, times the row's and the tokens' factors,
+// plus log2 of the value scales; -inf where the row does not look), and their maximum
+__device__ __forceinline__ float scores32(const uint32_t (&a)[32], const float *sk, const float *lv, float rf,
+                                          uint32_t vis, uint64_t (&z)[16])
+{
+    const uint64_t rf2 = pair(rf, rf);
 #pragma unroll
-    for (int t = 0; t < 32; t += 4) {
-        const float4 k = *reinterpret_cast<const float4 *>(sk + t), v = *reinterpret_cast<const float4 *>(lv + t);
-        z[t] = fmaf(__uint_as_float(r[t]) * k.x, rf, v.x);
-        z[t + 1] = fmaf(__uint_as_float(r[t + 1]) * k.y, rf, v.y);
-        z[t + 2] = fmaf(__uint_as_float(r[t + 2]) * k.z, rf, v.z);
-        z[t + 3] = fmaf(__uint_as_float(r[t + 3]) * k.w, rf, v.w);
+    for (int t = 0; t < 16; t += 2) {
+        const ulonglong2 k = *reinterpret_cast<const ulonglong2 *>(sk + 2 * t);
+        const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(lv + 2 * t);
+        z[t] = fma2(mul2(pair(a[2 * t], a[2 * t + 1]), k.x), rf2, v.x);
+        z[t + 1] = fma2(mul2(pair(a[2 * t + 2], a[2 * t + 3]), k.y), rf2, v.y);
     }
     if (vis != FULL) {
 #pragma unroll
-        for (int t = 0; t < 32; t++) z[t] = (vis >> t) & 1u ? z[t] : -INFINITY;
+        for (int t = 0; t < 16; t++)
+            z[t] = pair((vis >> (2 * t)) & 1u ? first(z[t]) : -INFINITY,
+                        (vis >> (2 * t + 1)) & 1u ? second(z[t]) : -INFINITY);
     }
+    float m0 = fmaxf(first(z[0]), second(z[0])), m1 = fmaxf(first(z[1]), second(z[1]));
+#pragma unroll
+    for (int t = 2; t < 16; t += 2) {
+        m0 = fmaxf(m0, fmaxf(first(z[t]), second(z[t])));
+        m1 = fmaxf(m1, fmaxf(first(z[t + 1]), second(z[t + 1])));
+    }
+    return fmaxf(m0, m1);
 }
 
-__device__ __forceinline__ float max32(const float *z, float m)
+// P = 2^(z - m) of 32 tokens, rounded to f16, into 16 packed columns; returns their share of l
+__device__ __forceinline__ float probs32(const uint64_t (&z)[16], const float *iv, float m, uint32_t (&w)[16])
 {
-    float a = fmaxf(z[0], z[1]), b = fmaxf(z[2], z[3]);
+    const uint64_t nm = pair(-m, -m);
+    uint64_t l0 = 0, l1 = 0;
 #pragma unroll
-    for (int t = 4; t < 32; t += 4) {
-        a = fmaxf(a, fmaxf(z[t], z[t + 1]));
-        b = fmaxf(b, fmaxf(z[t + 2], z[t + 3]));
+    for (int t = 0; t < 16; t += 2) {
+        const ulonglong2 i = *reinterpret_cast<const ulonglong2 *>(iv + 2 * t);
+        const uint64_t x = add2(z[t], nm), y = add2(z[t + 1], nm);
+        const float a = ex2(first(x)), b = ex2(second(x)), c = ex2(first(y)), d = ex2(second(y));
+        l0 = fma2(pair(a, b), i.x, l0);
+        l1 = fma2(pair(c, d), i.y, l1);
+        w[t] = pack_half2(a, b);
+        w[t + 1] = pack_half2(c, d);
     }
-    return fmaxf(m, fmaxf(a, b));
-}
-
-// P of 32 tokens into 16 packed columns, and their share of l
-__device__ __forceinline__ float probs32(const float *z, const float *iv, float m, uint32_t (&w)[16])
-{
-    float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-    for (int t = 0; t < 32; t += 4) {
-        const float4 i = *reinterpret_cast<const float4 *>(iv + t);
-        const float a = ex2(z[t] - m), b = ex2(z[t + 1] - m), c = ex2(z[t + 2] - m), d = ex2(z[t + 3] - m);
-        l0 = fmaf(a, i.x, l0);
-        l1 = fmaf(b, i.y, l1);
-        l0 = fmaf(c, i.z, l0);
-        l1 = fmaf(d, i.w, l1);
-        w[t / 2] = pack_half2(a, b);
-        w[t / 2 + 1] = pack_half2(c, d);
-    }
-    return l0 + l1;
+    return (first(l0) + second(l0)) + (first(l1) + second(l1));
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -513,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             const int ksb = DH / p.k.group * scale_vals(p.fmt) * 2, vsb = DH / p.v.group * scale_vals(p.fmt) * 2;
             Walk it;
             it.start(p, w);
-            int e = 0;
+            int e = 0, s = 0, use = 0;          // entries filled; the next one's place and use
             for (int i = 0; i < n_units && !*abort_flag; i++) {
                 const int head = it.inner / it.s.rtn, t0 = it.tile * TT;
                 const int nv = min(TT, it.s.total - t0);
@@ -527,9 +566,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 }
                 const int nsc = (nv + 7) & ~7;      // rows whose scales are whole 16-byte pieces
                 bool ok = true;
+#pragma unroll 1
                 for (int kv = 0; kv < 2; kv++, e++) {
-                    const int s = e % E;
-                    if (e >= E && !mbar_wait_bounded(&ctl->empty[s], (e / E - 1) & 1, abort_flag, limit)) {
+                    if (use > 0 && !mbar_wait_bounded(&ctl->empty[s], (use - 1) & 1, abort_flag, limit)) {
                         give_up();
                         ok = false;
                         break;
@@ -543,6 +582,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                     if (sc)
                         bulk_load_hint(dst + p.l.off_scales, reinterpret_cast<const uint8_t *>(t.scales) + row * sb,
                                        (uint32_t)(nsc * sb), &ctl->full[s], pol);
+                    if (++s == E) {
+                        s = 0;
+                        ++use;
+                    }
                 }
                 if (!ok) break;
                 it.next(p);
@@ -560,11 +603,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             int seg = -1;
             bool ok = true, first_prev = false;
             auto issue_pv = [&](int i, bool first) -> bool {
-                const int j = i & 1, vb = i % VB;
-                if (!mbar_wait_bounded(&ctl->vfull[vb], (i / VB) & 1, abort_flag, limit)) return false;
+                const int j = i & 1, vb = i & (VB - 1);
+                if (!mbar_wait_bounded(&ctl->vfull[vb], (i >> (VB - 1)) & 1, abort_flag, limit)) return false;
                 if (!mbar_wait_bounded(&ctl->pfull[j], (i >> 1) & 1, abort_flag, limit)) return false;
                 tc_fence_after();
                 const uint32_t v0 = sbase + p.l.off_v + (uint32_t)vb * p.l.v_bytes;
+#pragma unroll 1
                 for (int part = 0; part <= p.l.v_grouped; part++)
 #pragma unroll
                     for (int kk = 0; kk < TT / 16; kk++)
@@ -575,11 +619,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 return true;
             };
             auto issue_s = [&](int i) -> bool {
-                const int kb = i % KB;
-                if (!mbar_wait_bounded(&ctl->kfull[kb], (i / KB) & 1, abort_flag, limit)) return false;
+                const int kb = i & (KB - 1);
+                if (!mbar_wait_bounded(&ctl->kfull[kb], (i >> (KB - 1)) & 1, abort_flag, limit)) return false;
                 tc_fence_after();
                 const uint32_t k0 = sbase + p.l.off_k + (uint32_t)kb * p.l.k_bytes;
+#pragma unroll 1
                 for (int part = 0; part <= p.l.k_grouped; part++)
+#pragma unroll 1
                     for (int qp = 0; qp <= (q2 ? 1 : 0); qp++)
 #pragma unroll
                         for (int kk = 0; kk < DH / 16; kk++)
@@ -618,32 +664,36 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         Walk it;
         if (n_units > 0) it.start(p, w);
         bool ok = true;
+        int s = 0, use = 0;
         for (int i = 0; i < n_units && ok; i++) {
             const int nv = min(TT, it.s.total - it.tile * TT);
 #pragma unroll
             for (int kv = 0; kv < 2; kv++) {
-                const int e = 2 * i + kv, s = e % E;
-                ok = wait(&ctl->full[s], e / E);
+                ok = wait(&ctl->full[s], use);
                 if (!ok) break;
                 const uint8_t *entry = smem + (uint32_t)s * p.l.entry_bytes;
                 if (kv == 0) {
                     // the operand's last use: S of tile i - KB
                     if (i >= KB) ok = wait(&ctl->sfull[(i - KB) & 1], (i - KB) >> 1);
                     if (!ok) break;
-                    convert_any<DH, false>(p, entry, smem + p.l.off_k + (uint32_t)(i % KB) * p.l.k_bytes, nv, ct, kt,
+                    convert_any<DH, false>(p, entry, smem + p.l.off_k + (uint32_t)(i & (KB - 1)) * p.l.k_bytes, nv, ct, kt,
                                            par->sk[i & 3], nullptr);
                 } else {
                     if (i >= VB) ok = wait(&ctl->pvdone[(i - VB) & 1], (i - VB) >> 1);
                     if (!ok) break;
-                    convert_any<DH, true>(p, entry, smem + p.l.off_v + (uint32_t)(i % VB) * p.l.v_bytes, nv, ct, vt,
+                    convert_any<DH, true>(p, entry, smem + p.l.off_v + (uint32_t)(i & (VB - 1)) * p.l.v_bytes, nv, ct, vt,
                                           par->lv[i & 3], par->iv[i & 3]);
                 }
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(kv ? &ctl->vfull[i % VB] : &ctl->kfull[i % KB]);
+                    mbar_arrive(kv ? &ctl->vfull[i & (VB - 1)] : &ctl->kfull[i & (KB - 1)]);
                     mbar_arrive(&ctl->par[i & 3]);
                     mbar_arrive(&ctl->empty[s]);
+                }
+                if (++s == E) {
+                    s = 0;
+                    ++use;
                 }
             }
             if (ok) it.next(p);
@@ -668,12 +718,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         };
         float m = -INFINITY, l = 0.f, rf = 0.f;
         uint64_t mask = 0;
-        int rows = 0, copies = 1, r = 0, tb = 0;
+        int rows = 0, copies = 1, r = 0, tb = 0, seg0 = 0;
         for (int i = 0; i < n_units && ok; i++) {
             const int j = i & 1, t0 = it.tile * TT;
             const int head = it.inner / it.s.rtn, rt = it.inner % it.s.rtn;
             if (i == 0 || it.tile == 0) {
                 // ---- a segment starts: this thread's row, its mask, its query into TMEM
+                seg0 = i;
                 m = -INFINITY;
                 l = 0.f;
                 rows = min(kTreeRows, it.s.n * p.G - rt * kTreeRows);
@@ -714,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                         rf = p.tau_log2e * pow2i(ex);
                     }
                 }
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < DH / 32; c++) {
                     uint32_t hi[16], lo[16];
 #pragma unroll
@@ -771,88 +822,59 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             const uint32_t s_at = tmem + COL_S + 128u * j + lane_off;
             const float *sk = par->sk[i & 3] + tb, *lv = par->lv[i & 3] + tb, *iv = par->iv[i & 3] + tb;
             const bool whole = t0 + TT <= it.s.len;
-            auto vis = [&](int c) { return whole ? FULL : visible(t0 + tb + 32 * c, it.s.len, mask); };
-            // the maximum moved too far: raise m, and with it O and l
-            auto raise = [&](float mx) -> bool {
-                const bool set = m == -INFINITY && mx > -INFINITY;
-                const bool up = mx > m + kMoveAt && !set;
+            // one 32-token chunk at a time: its z, its maximum, its P over S's columns
+            const int chunks = 4 / copies;
+            const uint32_t p_at = s_at + (uint32_t)tb / 2;
+#pragma unroll 1
+            for (int c = 0; c < chunks && ok; c++) {
+                uint32_t a[32], pw[16];
+                uint64_t z[16];
+                tmem_ld32(s_at + tb + 32u * c, a);
+                const uint32_t vis = whole ? FULL : visible(t0 + tb + 32 * c, it.s.len, mask);
+                const float mx = scores32(a, sk + 32 * c, lv + 32 * c, rf, vis, z);
+                const bool set = m == -INFINITY && mx > -INFINITY, up = !set && mx > m + kMoveAt;
                 float alpha = 1.f;
                 if (set || up) {
-                    const float to = mx - kHead;
-                    if (up) alpha = ex2(m - to);
+                    const float to = floorf(mx) - kHead;
+                    if (up) alpha = ex2(m - to);             // m and to are whole: a power of two
                     m = to;
                     l *= alpha;
                 }
                 if (__any_sync(FULL, up)) {
-                    // (never in a segment's first tile: m is -inf there)
-                    if (!wait(&ctl->pvdone[j ^ 1], (i - 1) >> 1)) return false;
-                    tc_fence_after();
+                    // m moved too far for some row: O follows (every P V before this tile is in
+                    // it; in a segment's first tile there is nothing yet), and this tile's P
+                    if (i > seg0) {
+                        if (!(ok = wait(&ctl->pvdone[j ^ 1], (i - 1) >> 1))) break;
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int x = 0; x < DH / 32; x++) {
+                            tmem_ld32(tmem + COL_O + lane_off + 32u * x, a);
 #pragma unroll
-                    for (int c = 0; c < DH / 32; c++) {
-                        uint32_t o[32];
-                        tmem_ld32(tmem + COL_O + lane_off + 32u * c, o);
+                            for (int y = 0; y < 32; y++) a[y] = __float_as_uint(__uint_as_float(a[y]) * alpha);
+                            tmem_st32(tmem + COL_O + lane_off + 32u * x, a);
+                        }
+                    }
+                    const uint32_t alpha2 = pack_half2(alpha, alpha);
+#pragma unroll 1
+                    for (int x = 0; x < c; x++) {
+                        tmem_st_wait();
+                        tmem_ld16(p_at + 16u * x, pw);
 #pragma unroll
-                        for (int x = 0; x < 32; x++) o[x] = __float_as_uint(__uint_as_float(o[x]) * alpha);
-                        tmem_st32(tmem + COL_O + lane_off + 32u * c, o);
+                        for (int y = 0; y < 16; y++) pw[y] = hmul2_u32(pw[y], alpha2);
+                        tmem_st16(p_at + 16u * x, pw);
                     }
                 }
-                return true;
-            };
-            const float none = -INFINITY;
-            if (copies == 1) {
-                // all 128 tokens: too many scores for registers, so S is read twice
-                float z[32], mx = none;
+                l += probs32(z, iv + 32 * c, m == -INFINITY ? 0.f : m, pw);
+                tmem_st16(p_at + 16u * c, pw);
+            }
+            if (!ok) break;
+            if (copies > 1) {
+                // the other copies' tokens
+                uint32_t none[16];
 #pragma unroll
-                for (int c = 0; c < 4; c++) {
-                    uint32_t a[32];
-                    tmem_ld32(s_at + 32u * c, a);
-                    scores32(a, sk + 32 * c, lv + 32 * c, rf, vis(c), z);
-                    mx = max32(z, mx);
-                }
-                if (!(ok = raise(mx))) break;
-                const float me = m == -INFINITY ? 0.f : m;
-#pragma unroll
-                for (int c = 0; c < 4; c++) {
-                    uint32_t a[32], pw[16];
-                    tmem_ld32(s_at + 32u * c, a);
-                    scores32(a, sk + 32 * c, lv + 32 * c, rf, vis(c), z);
-                    l += probs32(z, iv + 32 * c, me, pw);
-                    tmem_st16(s_at + 16u * c, pw);
-                }
-            } else if (copies == 2) {
-                float z[64];
-                uint32_t a[32], pw[16];
-                tmem_ld32(s_at + tb, a);
-                scores32(a, sk, lv, rf, vis(0), z);
-                tmem_ld32(s_at + tb + 32u, a);
-                scores32(a, sk + 32, lv + 32, rf, vis(1), z + 32);
-                if (!(ok = raise(max32(z + 32, max32(z, none))))) break;
-                const float me = m == -INFINITY ? 0.f : m;
-#pragma unroll
-                for (int c = 0; c < 2; c++) {
-                    l += probs32(z + 32 * c, iv + 32 * c, me, pw);
-                    tmem_st16(s_at + (uint32_t)tb / 2 + 16u * c, pw);
-                }
-#pragma unroll
-                for (int x = 0; x < 16; x++) pw[x] = 0u;
-                tmem_st16(s_at + (32u - (uint32_t)tb / 2), pw);
-                tmem_st16(s_at + (32u - (uint32_t)tb / 2) + 16u, pw);
-            } else {
-                float z[32];
-                uint32_t a[32], pw[16], no[16];
-                tmem_ld32(s_at + tb, a);
-                scores32(a, sk, lv, rf, vis(0), z);
-                if (!(ok = raise(max32(z, none)))) break;
-                l += probs32(z, iv, m == -INFINITY ? 0.f : m, pw);
-#pragma unroll
-                for (int x = 0; x < 16; x++) no[x] = 0u;
-#pragma unroll
-                for (int c = 0; c < 4; c++) {
-                    if (c == warp)
-                        tmem_st16(s_at + 16u * c, pw);
-                    else
-                        tmem_st16(s_at + 16u * c, no);
-                }
+                for (int x = 0; x < 16; x++) none[x] = 0u;
+#pragma unroll 1
+                for (int c = chunks; c < 4; c++) tmem_st16(s_at + (((uint32_t)tb / 2 + 16u * c) & 63u), none);
             }
             tmem_st_wait();
             tc_fence_before();
