@@ -46,7 +46,7 @@ constexpr int TT = 128;                 // tokens of a tile
 constexpr int kSoftWarps = 4, kConvWarps = 8;
 constexpr int kProducerWarp = 4, kMmaWarp = 5, kConvWarp0 = 6;
 constexpr int kThreads = 32 * (kConvWarp0 + kConvWarps);
-constexpr int kConvThreads = 32 * kConvWarps;
+constexpr int kConvThreads = 16 * kConvWarps;   // of K, and of V
 constexpr int kMaxEntries = 12;
 constexpr unsigned FULL = 0xffffffffu;
 
@@ -89,6 +89,12 @@ __device__ __forceinline__ float lg2(float x)
     return y;
 }
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+
+// The loop of a wait whose first try failed, out of line: the roles' hot code has to stay small.
+__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, int *abort_flag, uint64_t limit)
+{
+    return mbar_wait_bounded(bar, parity, abort_flag, limit);
+}
 
 // ------------------------------------------------------------------ work split
 struct Seq {
@@ -280,6 +286,7 @@ __device__ __forceinline__ void convert(const uint8_t *raw, const uint16_t *sc, 
     // the lanes' loads hit all banks too.
     constexpr int ROW = DH / 8 * Raw<KIND>::BYTES, PANELS = DH / 64, RPP = kConvThreads / 8, PASSES = TT / RPP;
     constexpr int PAIR = KIND == K_ASYM ? 2 : 1;
+    static_assert(kConvThreads == TT, "a thread a token");
     // elements that are not numbers: dropped, and the token's queries told by log2 = NaN
     constexpr bool CHECK = ISV && (KIND == K_E4M3 || KIND == K_F16);
     const int c = ct & 7, tr = ct >> 3, lane = ct & 31;
@@ -305,13 +312,13 @@ __device__ __forceinline__ void convert(const uint8_t *raw, const uint16_t *sc, 
                 // P = 0 where the token is masked, so it has to be a number)
                 if (s == 0.f || bad || t >= nvalid) s = 1.f;
                 p0[t] = bad ? __int_as_float(0x7fc00000) : lg2(s);
-                p1[t] = 1.f / s;
+                p1[t] = __frcp_rn(s);
             } else {
                 p0[t] = s;
             }
         }
     };
-    if (!CHECK && ct < TT) params(ct, false);
+    if (!CHECK) params(ct, false);                             // a thread a token
 
     const uint8_t *src = raw + tr * ROW + c * Raw<KIND>::BYTES;
     uint8_t *out = dst + tr * 128 + ((c ^ tr) & 7) * 16;      // (t ^ tr) & 7 = 0: RPP is a multiple of 8
@@ -497,32 +504,35 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     Ctl *ctl = reinterpret_cast<Ctl *>(smem + p.l.off_ctl);
     Par *par = reinterpret_cast<Par *>(smem + p.l.off_par);
-    volatile int *abort_flag = &ctl->abort;
+    int *abort_flag = &ctl->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int E = p.l.entries, KB = p.l.k_bufs, VB = p.l.v_bufs;
     const uint64_t limit = p.timeout_ns;
     auto give_up = [&]() {
-        *abort_flag = 1;
+        *static_cast<volatile int *>(abort_flag) = 1;
         atomicExch(p.status, KVQ_ERR_TIMEOUT);
+    };
+    auto wait1 = [&](uint64_t *bar, int parity) {
+        return mbar_try_wait(bar, parity & 1) || wait_slow(bar, parity & 1, abort_flag, limit);
     };
     // a wait of a whole warp: its lanes go on, or give up, together
     auto wait = [&](uint64_t *bar, int parity) {
-        return __all_sync(FULL, mbar_wait_bounded(bar, parity & 1, abort_flag, limit)) != 0;
+        return __all_sync(FULL, wait1(bar, parity)) != 0;
     };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < E; s++) {
             mbar_init(&ctl->full[s], 1);
-            mbar_init(&ctl->empty[s], kConvWarps);
+            mbar_init(&ctl->empty[s], kConvWarps / 2);
         }
         for (int j = 0; j < 2; j++) {
-            mbar_init(&ctl->kfull[j], kConvWarps);
-            mbar_init(&ctl->vfull[j], kConvWarps);
+            mbar_init(&ctl->kfull[j], kConvWarps / 2);
+            mbar_init(&ctl->vfull[j], kConvWarps / 2);
             mbar_init(&ctl->sfull[j], 1);
             mbar_init(&ctl->pfull[j], kSoftWarps);
             mbar_init(&ctl->pvdone[j], 1);
         }
-        for (int j = 0; j < 4; j++) mbar_init(&ctl->par[j], 2 * kConvWarps);
+        for (int j = 0; j < 4; j++) mbar_init(&ctl->par[j], kConvWarps);
         mbar_init(&ctl->qfull, kSoftWarps);
         mbar_init(&ctl->soft, kSoftWarps);
         mbar_init(&ctl->drain, 1);
@@ -553,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             Walk it;
             it.start(p, w);
             int e = 0, s = 0, use = 0;          // entries filled; the next one's place and use
-            for (int i = 0; i < n_units && !*abort_flag; i++) {
+            for (int i = 0; i < n_units; i++) {
                 const int head = it.inner / it.s.rtn, t0 = it.tile * TT;
                 const int nv = min(TT, it.s.total - t0);
                 int64_t row;
@@ -568,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 bool ok = true;
 #pragma unroll 1
                 for (int kv = 0; kv < 2; kv++, e++) {
-                    if (use > 0 && !mbar_wait_bounded(&ctl->empty[s], (use - 1) & 1, abort_flag, limit)) {
+                    if (use > 0 && !wait1(&ctl->empty[s], use - 1)) {
                         give_up();
                         ok = false;
                         break;
@@ -604,8 +614,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             bool ok = true, first_prev = false;
             auto issue_pv = [&](int i, bool first) -> bool {
                 const int j = i & 1, vb = i & (VB - 1);
-                if (!mbar_wait_bounded(&ctl->vfull[vb], (i >> (VB - 1)) & 1, abort_flag, limit)) return false;
-                if (!mbar_wait_bounded(&ctl->pfull[j], (i >> 1) & 1, abort_flag, limit)) return false;
+                if (!wait1(&ctl->vfull[vb], i >> (VB - 1))) return false;
+                if (!wait1(&ctl->pfull[j], i >> 1)) return false;
                 tc_fence_after();
                 const uint32_t v0 = sbase + p.l.off_v + (uint32_t)vb * p.l.v_bytes;
 #pragma unroll 1
@@ -620,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             };
             auto issue_s = [&](int i) -> bool {
                 const int kb = i & (KB - 1);
-                if (!mbar_wait_bounded(&ctl->kfull[kb], (i >> (KB - 1)) & 1, abort_flag, limit)) return false;
+                if (!wait1(&ctl->kfull[kb], i >> (KB - 1))) return false;
                 tc_fence_after();
                 const uint32_t k0 = sbase + p.l.off_k + (uint32_t)kb * p.l.k_bytes;
 #pragma unroll 1
@@ -641,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 const bool first = have && (i == 0 || it.tile == 0);
                 // a new segment's queries replace the old ones: its scores wait for the last P V
                 if (i > 0 && (first || !have)) ok = issue_pv(i - 1, first_prev);
-                if (ok && first) ok = mbar_wait_bounded(&ctl->qfull, (++seg) & 1, abort_flag, limit);
+                if (ok && first) ok = wait1(&ctl->qfull, ++seg);
                 if (ok && have) {
                     ok = issue_s(i);
                     issued |= ok;
@@ -658,45 +668,46 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         }
     } else if (warp >= kConvWarp0) {
         // ====================== converters ======================
-        const int ct = threadIdx.x - 32 * kConvWarp0;
-        const bool pt = p.fmt == KVQ_FMT_TENSOR;
-        const float kt = pt ? __half2float(p.k.scales[0]) : 1.f, vt = pt ? __half2float(p.v.scales[0]) : 1.f;
+        // four warps turn K tiles, four V tiles
+        const int kv = warp >= kConvWarp0 + kConvWarps / 2;
+        const int ct = (threadIdx.x - 32 * kConvWarp0) & (kConvThreads - 1);
+        const CacheTensor &t = kv ? p.v : p.k;
+        const float tensor = p.fmt == KVQ_FMT_TENSOR ? __half2float(t.scales[0]) : 1.f;
+        const int bufs = kv ? VB : KB;
+        uint8_t *tiles = smem + (kv ? p.l.off_v : p.l.off_k);
+        const uint32_t tile_bytes = kv ? p.l.v_bytes : p.l.k_bytes;
+        uint64_t *ready = kv ? ctl->vfull : ctl->kfull, *used = kv ? ctl->pvdone : ctl->sfull;
         Walk it;
         if (n_units > 0) it.start(p, w);
         bool ok = true;
-        int s = 0, use = 0;
-        for (int i = 0; i < n_units && ok; i++) {
+        int s = kv, use = 0;
+        for (int i = 0; i < n_units; i++) {
             const int nv = min(TT, it.s.total - it.tile * TT);
-#pragma unroll
-            for (int kv = 0; kv < 2; kv++) {
-                ok = wait(&ctl->full[s], use);
-                if (!ok) break;
-                const uint8_t *entry = smem + (uint32_t)s * p.l.entry_bytes;
-                if (kv == 0) {
-                    // the operand's last use: S of tile i - KB
-                    if (i >= KB) ok = wait(&ctl->sfull[(i - KB) & 1], (i - KB) >> 1);
-                    if (!ok) break;
-                    convert_any<DH, false>(p, entry, smem + p.l.off_k + (uint32_t)(i & (KB - 1)) * p.l.k_bytes, nv, ct, kt,
-                                           par->sk[i & 3], nullptr);
-                } else {
-                    if (i >= VB) ok = wait(&ctl->pvdone[(i - VB) & 1], (i - VB) >> 1);
-                    if (!ok) break;
-                    convert_any<DH, true>(p, entry, smem + p.l.off_v + (uint32_t)(i & (VB - 1)) * p.l.v_bytes, nv, ct, vt,
-                                          par->lv[i & 3], par->iv[i & 3]);
-                }
-                fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(kv ? &ctl->vfull[i & (VB - 1)] : &ctl->kfull[i & (KB - 1)]);
-                    mbar_arrive(&ctl->par[i & 3]);
-                    mbar_arrive(&ctl->empty[s]);
-                }
-                if (++s == E) {
-                    s = 0;
-                    ++use;
-                }
+            ok = wait(&ctl->full[s], use);
+            // the operand's last use: S, or P V, of tile i - bufs
+            if (ok && i >= bufs) ok = wait(&used[(i - bufs) & 1], (i - bufs) >> 1);
+            if (!ok) break;
+            const uint8_t *entry = smem + (uint32_t)s * p.l.entry_bytes;
+            const int buf = i & (bufs - 1);
+            if (kv)
+                convert_any<DH, true>(p, entry, tiles + (uint32_t)buf * tile_bytes, nv, ct, tensor, par->lv[i & 3],
+                                      par->iv[i & 3]);
+            else
+                convert_any<DH, false>(p, entry, tiles + (uint32_t)buf * tile_bytes, nv, ct, tensor, par->sk[i & 3],
+                                       nullptr);
+            fence_proxy_async_shared();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&ctl->par[i & 3]);       // before the tile can be used, so that its
+                mbar_arrive(&ready[buf]);            // phase is over when the slot comes round
+                mbar_arrive(&ctl->empty[s]);
             }
-            if (ok) it.next(p);
+            s += 2;
+            if (s >= E) {
+                s -= E;
+                ++use;
+            }
+            it.next(p);
         }
         if (!ok) give_up();
     } else {
@@ -716,103 +727,101 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             ++syncs;
             return r;
         };
-        float m = -INFINITY, l = 0.f, rf = 0.f;
-        uint64_t mask = 0;
-        int rows = 0, copies = 1, r = 0, tb = 0, seg0 = 0;
-        for (int i = 0; i < n_units && ok; i++) {
-            const int j = i & 1, t0 = it.tile * TT;
-            const int head = it.inner / it.s.rtn, rt = it.inner % it.s.rtn;
-            if (i == 0 || it.tile == 0) {
-                // ---- a segment starts: this thread's row, its mask, its query into TMEM
-                seg0 = i;
-                m = -INFINITY;
-                l = 0.f;
-                rows = min(kTreeRows, it.s.n * p.G - rt * kTreeRows);
-                copies = rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
-                r = place & (TT / copies - 1);
-                tb = place - r;
-                const int rr = rt * kTreeRows + r, qi = rr / p.G;
-                const bool live = r < rows;
-                mask = 0;
-                if (live) {
-                    mask = p.d_mask ? p.d_mask[(int64_t)it.b * p.n_tree + qi] : ~0ull >> (63 - qi);
-                    const int nd = it.s.total - it.s.len;            // drafted tokens that exist
-                    mask &= nd > 0 ? ~0ull >> (64 - nd) : 0ull;
-                }
-                const int64_t at = (((int64_t)it.b * p.n_tree + qi) * p.n_q_heads + (int64_t)head * p.G + rr % p.G) * DH;
-                rf = p.tau_log2e;
-                float pre = 1.f;
-                if (p.q_dtype != KVQ_F16) {
-                    // bring the row's largest element to [2^8, 2^9): f16 then holds bf16 elements
-                    // (and the first part of fp32 ones) as they are
+        // What a thread keeps of its row; the next segment's is made while the last tile of the
+        // current one is with the tensor cores.
+        struct Row {
+            int rows, copies, tb;                    // rows of the tile, their copies; first token of this copy
+            float rf;                                // factor of a score: tau log2(e), the query's power of two
+            uint64_t mask;                           // drafted tokens that the row attends
+        };
+        // this thread's row of the walk's segment, its query into TMEM
+        auto open = [&](const Walk &o) {
+            const int head = o.inner / o.s.rtn, rt = o.inner % o.s.rtn;
+            Row x;
+            x.rows = min(kTreeRows, o.s.n * p.G - rt * kTreeRows);
+            x.copies = x.rows <= 32 ? 4 : x.rows <= 64 ? 2 : 1;
+            const int r = place & (TT / x.copies - 1);
+            x.tb = place - r;
+            const int rr = rt * kTreeRows + r, qi = rr / p.G;
+            const bool live = r < x.rows;
+            const int64_t at = (((int64_t)o.b * p.n_tree + qi) * p.n_q_heads + (int64_t)head * p.G + rr % p.G) * DH;
+            x.rf = p.tau_log2e;
+            x.mask = 0;
+            if (live) {
+                const int nd = o.s.total - o.s.len;                  // drafted tokens that exist
+                x.mask = p.d_mask ? p.d_mask[(int64_t)o.b * p.n_tree + qi] : ~0ull >> (63 - qi);
+                x.mask &= nd > 0 ? ~0ull >> (64 - nd) : 0ull;
+            }
+            // bring the largest element of a row to [2^8, 2^9): f16 then holds bf16 elements, and
+            // the first part of fp32 ones, as they are
+            auto level = [&](float a) {
+                if (!(a > 0.f && a < INFINITY)) return 1.f;
+                const int ex = max((__float_as_int(a) >> 23) - 127, -110) - 8;
+                x.rf = p.tau_log2e * pow2i(ex);
+                return pow2i(-ex);
+            };
+            if (p.q_dtype != KVQ_F32) {
+                uint4 u[DH / 8];
+                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + at);
+#pragma unroll
+                for (int k = 0; k < DH / 8; k++) u[k] = live ? src[k] : make_uint4(0u, 0u, 0u, 0u);
+                uint32_t *h = reinterpret_cast<uint32_t *>(u);
+                if (p.q_dtype == KVQ_BF16) {
                     float a = 0.f;
-                    if (live)
-                        for (int d = 0; d < DH; d += 4) {
-                            float x[4];
-                            if (p.q_dtype == KVQ_F32) {
-                                const float4 f = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + at + d);
-                                x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
-                            } else {
-                                const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p.q) + at + d);
-                                x[0] = __uint_as_float(u.x << 16); x[1] = __uint_as_float(u.x & 0xffff0000u);
-                                x[2] = __uint_as_float(u.y << 16); x[3] = __uint_as_float(u.y & 0xffff0000u);
-                            }
-                            a = fmaxf(fmaxf(a, fmaxf(fabsf(x[0]), fabsf(x[1]))), fmaxf(fabsf(x[2]), fabsf(x[3])));
-                        }
-                    if (a > 0.f && a < INFINITY) {
-                        const int ex = max((__float_as_int(a) >> 23) - 127, -110) - 8;
-                        pre = pow2i(-ex);
-                        rf = p.tau_log2e * pow2i(ex);
-                    }
+#pragma unroll
+                    for (int k = 0; k < DH / 2; k++)
+                        a = fmaxf(a, fmaxf(fabsf(__uint_as_float(h[k] << 16)), fabsf(__uint_as_float(h[k] & 0xffff0000u))));
+                    const float pre = level(a);
+#pragma unroll
+                    for (int k = 0; k < DH / 2; k++)
+                        h[k] = pack_half2(__uint_as_float(h[k] << 16) * pre, __uint_as_float(h[k] & 0xffff0000u) * pre);
                 }
+#pragma unroll
+                for (int k = 0; k < DH / 32; k++)
+                    tmem_st16(tmem + COL_Q + lane_off + 16u * k, *reinterpret_cast<uint32_t(*)[16]>(h + 16 * k));
+            } else {
+                const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + at);
+                const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+                float a = 0.f;
+#pragma unroll 4
+                for (int k = 0; k < DH / 4; k++) {
+                    const float4 f = live ? src[k] : none;
+                    a = fmaxf(fmaxf(a, fmaxf(fabsf(f.x), fabsf(f.y))), fmaxf(fabsf(f.z), fabsf(f.w)));
+                }
+                const float pre = level(a);
 #pragma unroll 1
                 for (int c = 0; c < DH / 32; c++) {
                     uint32_t hi[16], lo[16];
 #pragma unroll
-                    for (int d = 0; d < 32; d += 8) {
-                        uint4 u = make_uint4(0u, 0u, 0u, 0u), v = u;
-                        if (live) {
-                            if (p.q_dtype == KVQ_F32) {
-                                const uint4 *f = reinterpret_cast<const uint4 *>(static_cast<const float *>(p.q) + at + 32 * c + d);
-                                u = f[0];
-                                v = f[1];
-                            } else {
-                                u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + at + 32 * c + d);
-                            }
-                        }
-                        float x[8];
-                        if (p.q_dtype == KVQ_F32) {
-                            x[0] = __uint_as_float(u.x); x[1] = __uint_as_float(u.y);
-                            x[2] = __uint_as_float(u.z); x[3] = __uint_as_float(u.w);
-                            x[4] = __uint_as_float(v.x); x[5] = __uint_as_float(v.y);
-                            x[6] = __uint_as_float(v.z); x[7] = __uint_as_float(v.w);
-                        } else {
-                            const uint32_t ww[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                            for (int k = 0; k < 4; k++) {
-                                x[2 * k] = __uint_as_float(ww[k] << 16);
-                                x[2 * k + 1] = __uint_as_float(ww[k] & 0xffff0000u);
-                            }
-                            v = u;
-                        }
-                        const uint32_t raw[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                        for (int k = 0; k < 4; k++) {
-                            const float a = x[2 * k] * pre, b = x[2 * k + 1] * pre;
-                            const uint32_t h = p.q_dtype == KVQ_F16 ? raw[k] : pack_half2(a, b);
-                            const float2 back = unpack_half2(h);
-                            hi[d / 2 + k] = h;
-                            lo[d / 2 + k] = pack_half2(a - back.x, b - back.y);
-                        }
+                    for (int k = 0; k < 8; k++) {
+                        float4 f = live ? src[8 * c + k] : none;
+                        f.x *= pre; f.y *= pre; f.z *= pre; f.w *= pre;
+                        hi[2 * k] = pack_half2(f.x, f.y);
+                        hi[2 * k + 1] = pack_half2(f.z, f.w);
+                        const float2 b0 = unpack_half2(hi[2 * k]), b1 = unpack_half2(hi[2 * k + 1]);
+                        lo[2 * k] = pack_half2(f.x - b0.x, f.y - b0.y);
+                        lo[2 * k + 1] = pack_half2(f.z - b1.x, f.w - b1.y);
                     }
                     tmem_st16(tmem + COL_Q + lane_off + 16u * c, hi);
-                    if (p.q_dtype == KVQ_F32) tmem_st16(tmem + COL_QLO + lane_off + 16u * c, lo);
+                    tmem_st16(tmem + COL_QLO + lane_off + 16u * c, lo);
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->qfull);
             }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->qfull);
+            return x;
+        };
+        float m = -INFINITY, l = 0.f;
+        int seg0 = 0;                                // the segment's first unit in this CTA
+        Row row{}, next{};
+        if (n_units > 0) row = open(it);
+        for (int i = 0; i < n_units; i++) {
+            const int j = i & 1, t0 = it.tile * TT;
+            const int copies = row.copies, tb = row.tb;
+            const bool last = i == n_units - 1 || it.tile == it.s.tiles - 1;
+            Walk ahead = it;
+            ahead.next(p);
 
             // ---- scores of the tile
             ok = wait(&ctl->par[i & 3], i >> 2) &&
@@ -826,12 +835,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             const int chunks = 4 / copies;
             const uint32_t p_at = s_at + (uint32_t)tb / 2;
 #pragma unroll 1
-            for (int c = 0; c < chunks && ok; c++) {
+            for (int c = 0; c < chunks; c++) {
                 uint32_t a[32], pw[16];
                 uint64_t z[16];
                 tmem_ld32(s_at + tb + 32u * c, a);
-                const uint32_t vis = whole ? FULL : visible(t0 + tb + 32 * c, it.s.len, mask);
-                const float mx = scores32(a, sk + 32 * c, lv + 32 * c, rf, vis, z);
+                const uint32_t vis = whole ? FULL : visible(t0 + tb + 32 * c, it.s.len, row.mask);
+                const float mx = scores32(a, sk + 32 * c, lv + 32 * c, row.rf, vis, z);
                 const bool set = m == -INFINITY && mx > -INFINITY, up = !set && mx > m + kMoveAt;
                 float alpha = 1.f;
                 if (set || up) {
@@ -880,19 +889,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->pfull[j]);
+            // every score of the segment is done: the next one's queries may come in
+            if (last && i + 1 < n_units) next = open(ahead);
 
             // ---- the segment's last tile: join the copies, write the output or a partial
-            if (i == n_units - 1 || it.tile == it.s.tiles - 1) {
-                const int nr = TT / copies;
-                ctl->ml[place] = make_float2(m, l);
-                ok = soft_sync() && wait(&ctl->pvdone[j], i >> 1);
-                if (!ok) break;
-                tc_fence_after();
-                float M = -INFINITY, L = 0.f;
-                for (int c = 0; c < copies; c++) M = fmaxf(M, ctl->ml[c * nr + r].x);
-                for (int c = 0; c < copies; c++) {
-                    const float2 x = ctl->ml[c * nr + r];
-                    L += x.x == -INFINITY ? 0.f : x.y * ex2(x.x - M);
+            if (last) {
+                const int head = it.inner / it.s.rtn, rt = it.inner % it.s.rtn;
+                const int nr = TT / copies, r = place - tb, rows = row.rows;
+                float M = m, L = l;
+                if (copies > 1) {
+                    ctl->ml[place] = make_float2(m, l);
+                    if (!(ok = soft_sync())) break;
+                    M = -INFINITY;
+                    L = 0.f;
+                    for (int c = 0; c < copies; c++) M = fmaxf(M, ctl->ml[c * nr + r].x);
+                    for (int c = 0; c < copies; c++) {
+                        const float2 x = ctl->ml[c * nr + r];
+                        L += x.x == -INFINITY ? 0.f : x.y * ex2(x.x - M);
+                    }
                 }
                 float f = m == -INFINITY ? 0.f : ex2(m - M) * osign;
                 const long long u0 = w.u0 + i - it.tile;
@@ -906,34 +920,54 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                     p.seg[((int64_t)it.b * p.rows.heads + head) * p.row_tiles + rt] = make_int4(slot, ca, cb - ca + 1, 0);
                 if (!direct && place < rows)
                     *reinterpret_cast<float2 *>(part + (int64_t)p.slot_rows * DH + 2 * place) = make_float2(M, L);
+                // columns col .. col + 3 of a row of the tile
+                auto put = [&](int rr, int col, const float (&y)[4]) {
+                    if (!direct) {
+                        *reinterpret_cast<float4 *>(part + (int64_t)rr * DH + col) = make_float4(y[0], y[1], y[2], y[3]);
+                        return;
+                    }
+                    rr += rt * kTreeRows;
+                    store4(p.out, (((int64_t)it.b * p.n_tree + rr / p.G) * p.n_q_heads + (int64_t)head * p.G + rr % p.G) * DH + col,
+                           p.out_dtype, y);
+                };
+                if (!(ok = wait(&ctl->pvdone[j], i >> 1))) break;
+                tc_fence_after();
 #pragma unroll 1
                 for (int c = 0; c < DH / 32; c++) {
                     uint32_t o[32];
                     tmem_ld32(tmem + COL_O + lane_off + 32u * c, o);
+                    if (copies == 1) {
+                        if (place < rows)
+#pragma unroll
+                            for (int x = 0; x < 32; x += 4) {
+                                float y[4];
+#pragma unroll
+                                for (int d = 0; d < 4; d++) y[d] = f == 0.f ? 0.f : __uint_as_float(o[x + d]) * f;
+                                put(place, 32 * c + x, y);
+                            }
+                        continue;
+                    }
                     if (c > 0 && !(ok = soft_sync())) break;         // the staging was read
 #pragma unroll
                     for (int x = 0; x < 32; x++) stage[place * STAGE_LD + x] = f == 0.f ? 0.f : __uint_as_float(o[x]) * f;
                     if (!(ok = soft_sync())) break;
+#pragma unroll 1
                     for (int x = place; x < rows * 8; x += TT) {
-                        const int row = x >> 3, col = (x & 7) * 4;
+                        const int rr = x >> 3, col = (x & 7) * 4;
                         float y[4] = {0.f, 0.f, 0.f, 0.f};
                         for (int k = 0; k < copies; k++)
 #pragma unroll
-                            for (int d = 0; d < 4; d++) y[d] += stage[(k * nr + row) * STAGE_LD + col + d];
-                        if (!direct) {
-                            *reinterpret_cast<float4 *>(part + (int64_t)row * DH + 32 * c + col) =
-                                make_float4(y[0], y[1], y[2], y[3]);
-                            continue;
-                        }
-                        const int rr = rt * kTreeRows + row;
-                        const int64_t at = (((int64_t)it.b * p.n_tree + rr / p.G) * p.n_q_heads + (int64_t)head * p.G +
-                                            rr % p.G) * DH + 32 * c + col;
-                        store4(p.out, at, p.out_dtype, y);
+                            for (int d = 0; d < 4; d++) y[d] += stage[(k * nr + rr) * STAGE_LD + col + d];
+                        put(rr, 32 * c + col, y);
                     }
                 }
                 if (!ok) break;
+                row = next;
+                m = -INFINITY;
+                l = 0.f;
+                seg0 = i + 1;
             }
-            it.next(p);
+            it = ahead;
         }
         if (!ok) give_up();
     }
