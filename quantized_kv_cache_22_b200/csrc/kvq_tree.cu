@@ -43,14 +43,24 @@ namespace kvq {
 namespace {
 
 constexpr int TT = 128;                 // tokens of a tile
-constexpr int kSoftWarps = 4, kConvWarps = 8;
-constexpr int kProducerWarp = 4, kMmaWarp = 5, kConvWarp0 = 6;
+constexpr int HT = TT / 2;               // tokens of a tile that one softmax group takes
+constexpr int kSoftWarps = 4, kConvWarps = 8;   // a softmax group's warps; converter warps
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kConvWarp0 = 12;   // (10 and 11 fill up their warpgroup)
 constexpr int kThreads = 32 * (kConvWarp0 + kConvWarps);
 constexpr int kConvThreads = 16 * kConvWarps;   // of K, and of V
 constexpr int kMaxEntries = 12;
 constexpr unsigned FULL = 0xffffffffu;
 
-constexpr uint32_t COL_S = 0, COL_O = 256, COL_Q = 384, COL_QLO = 448;   // TMEM columns
+// Registers a thread: the block starts with 96 x 640 threads and shares them out anew by
+// warpgroup (2 x softmax, producer and issuer, 2 x converters: 480 in all, as launched).
+constexpr int kSoftRegs = 128, kIssueRegs = 64, kConvRegs = 80;
+static_assert(2 * kSoftRegs + kIssueRegs + 2 * kConvRegs == 5 * 96, "the shares add up to the launch");
+template <int N>
+__device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void fewer_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+constexpr uint32_t COL_S = 0, COL_O = 128, COL_Q = 384, COL_QLO = 448;   // TMEM columns; S, O: two groups
 constexpr uint32_t PANEL = TT * 128;    // 64 f16 of every token
 
 // P in [0, 2^14]: m starts 6 to 7 below the first chunk's maximum and follows when 14 is passed
@@ -63,18 +73,19 @@ struct Work {
 };
 struct Ctl {
     uint64_t full[kMaxEntries], empty[kMaxEntries];
-    uint64_t kfull[2], vfull[2], sfull[2], pfull[2], pvdone[2], par[4], qfull, soft, drain;
+    uint64_t kfull[2], vfull[2], sfull[2][2], pfull[2][2], pvdone[2][2], par[4], qfull, soft, drain;
     Work w;
     uint32_t tmem;
     int abort;
-    float2 ml[TT];
+    float2 ml[2][TT];
 };
 // Per-token numbers of a tile, four tiles deep: the converters run at most two tiles ahead of
 // the softmax.
 struct Par {
     float sk[4][TT], lv[4][TT], iv[4][TT];
 };
-constexpr int STAGE_LD = 33;            // floats per row of the epilogue's 32-column staging
+constexpr int STAGE_LD = 17;            // floats per row of the epilogue's 16-column staging
+constexpr int STAGE_BYTES = 2 * TT * STAGE_LD * 4;
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -89,12 +100,6 @@ __device__ __forceinline__ float lg2(float x)
     return y;
 }
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
-
-// The loop of a wait whose first try failed, out of line: the roles' hot code has to stay small.
-__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, int *abort_flag, uint64_t limit)
-{
-    return mbar_wait_bounded(bar, parity, abort_flag, limit);
-}
 
 // ------------------------------------------------------------------ work split
 struct Seq {
@@ -122,6 +127,7 @@ __device__ void find_work(const TreeParams &p, int lane, Work &w)
 {
     const int Hkv = p.rows.heads, B = p.rows.batch;
     long long n = 0;
+#pragma unroll 1
     for (int b = lane; b < B; b += 32) {
         const Seq s = sequence(p, b);
         n += (long long)s.tiles * s.rtn * Hkv;
@@ -135,6 +141,7 @@ __device__ void find_work(const TreeParams &p, int lane, Work &w)
     }
     int fb = 0;
     long long pre = 0, acc = 0;
+#pragma unroll 1
     for (int b0 = 0; b0 < B && u1 > u0; b0 += 32) {
         const int b = b0 + lane;
         long long units = 0;
@@ -167,28 +174,42 @@ __device__ void find_work(const TreeParams &p, int lane, Work &w)
     }
 }
 
-// Walks the units of the CTA; every role keeps its own.
+// Walks the segments of the CTA: the tiles of one (sequence, KV head, row tile) that are its
+// own.  Every role keeps its own walk, so that nothing but tiles passes between them.
 struct Walk {
-    int b, inner, tile;                 // inner = KV head * row tiles + row tile
+    int b, head, rt;                    // sequence, KV head, row tile
+    int tile, count, left;              // first token tile, tiles of the segment, units left with it
     Seq s;
     __device__ __forceinline__ void start(const TreeParams &p, const Work &w)
     {
+        left = w.n_units;
+        count = 0;
+        if (left == 0) return;
         b = w.b;
         s = sequence(p, b);
-        const int off = (int)(w.u0 - w.pre);
-        inner = off / s.tiles;
-        tile = off % s.tiles;
+        const int off = (int)(w.u0 - w.pre), inner = off / s.tiles;
+        tile = off - inner * s.tiles;
+        head = inner / s.rtn;
+        rt = inner - head * s.rtn;
+        count = min(s.tiles - tile, left);
     }
+    // the next segment; count 0: none is left
     __device__ __forceinline__ void next(const TreeParams &p)
     {
-        if (++tile < s.tiles) return;
+        left -= count;
+        count = 0;
+        if (left == 0) return;
         tile = 0;
-        if (++inner < p.rows.heads * s.rtn) return;
-        inner = 0;
-        while (++b < p.rows.batch) {
-            s = sequence(p, b);
-            if (s.tiles) return;
+        if (++rt == s.rtn) {
+            rt = 0;
+            if (++head == p.rows.heads) {
+                head = 0;
+#pragma unroll 1
+                do s = sequence(p, ++b);
+                while (s.tiles == 0);
+            }
         }
+        count = min(s.tiles, left);
     }
 };
 
@@ -448,14 +469,15 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
     return r;
 }
 
-// z of 32 tokens (scores, fp32 accumulators in a, times the row's and the tokens' factors,
+// z of N tokens (scores, fp32 accumulators in a, times the row's and the tokens' factors,
 // plus log2 of the value scales; -inf where the row does not look), and their maximum
-__device__ __forceinline__ float scores32(const uint32_t (&a)[32], const float *sk, const float *lv, float rf,
-                                          uint32_t vis, uint64_t (&z)[16])
+template <int N>
+__device__ __forceinline__ float scores(const uint32_t (&a)[N], const float *sk, const float *lv, float rf,
+                                        uint32_t vis, uint64_t (&z)[N / 2])
 {
     const uint64_t rf2 = pair(rf, rf);
 #pragma unroll
-    for (int t = 0; t < 16; t += 2) {
+    for (int t = 0; t < N / 2; t += 2) {
         const ulonglong2 k = *reinterpret_cast<const ulonglong2 *>(sk + 2 * t);
         const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(lv + 2 * t);
         z[t] = fma2(mul2(pair(a[2 * t], a[2 * t + 1]), k.x), rf2, v.x);
@@ -463,26 +485,27 @@ __device__ __forceinline__ float scores32(const uint32_t (&a)[32], const float *
     }
     if (vis != FULL) {
 #pragma unroll
-        for (int t = 0; t < 16; t++)
+        for (int t = 0; t < N / 2; t++)
             z[t] = pair((vis >> (2 * t)) & 1u ? first(z[t]) : -INFINITY,
                         (vis >> (2 * t + 1)) & 1u ? second(z[t]) : -INFINITY);
     }
     float m0 = fmaxf(first(z[0]), second(z[0])), m1 = fmaxf(first(z[1]), second(z[1]));
 #pragma unroll
-    for (int t = 2; t < 16; t += 2) {
+    for (int t = 2; t < N / 2; t += 2) {
         m0 = fmaxf(m0, fmaxf(first(z[t]), second(z[t])));
         m1 = fmaxf(m1, fmaxf(first(z[t + 1]), second(z[t + 1])));
     }
     return fmaxf(m0, m1);
 }
 
-// P = 2^(z - m) of 32 tokens, rounded to f16, into 16 packed columns; returns their share of l
-__device__ __forceinline__ float probs32(const uint64_t (&z)[16], const float *iv, float m, uint32_t (&w)[16])
+// P = 2^(z - m) of N tokens, rounded to f16, into N / 2 packed columns; returns their share of l
+template <int N>
+__device__ __forceinline__ float probs(const uint64_t (&z)[N / 2], const float *iv, float m, uint32_t (&w)[N / 2])
 {
     const uint64_t nm = pair(-m, -m);
     uint64_t l0 = 0, l1 = 0;
 #pragma unroll
-    for (int t = 0; t < 16; t += 2) {
+    for (int t = 0; t < N / 2; t += 2) {
         const ulonglong2 i = *reinterpret_cast<const ulonglong2 *>(iv + 2 * t);
         const uint64_t x = add2(z[t], nm), y = add2(z[t + 1], nm);
         const float a = ex2(first(x)), b = ex2(second(x)), c = ex2(first(y)), d = ex2(second(y));
@@ -498,7 +521,7 @@ __device__ __forceinline__ float probs32(const uint64_t (&z)[16], const float *i
 template <int DH>
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p)
 {
-    constexpr uint32_t IDESC_S = (1u << 4) | ((uint32_t)(TT >> 3) << 17) | ((128u >> 4) << 24);
+    constexpr uint32_t IDESC_S = (1u << 4) | ((uint32_t)(HT >> 3) << 17) | ((128u >> 4) << 24);
     constexpr uint32_t IDESC_O = (1u << 4) | (1u << 16) | ((uint32_t)(DH >> 3) << 17) | ((128u >> 4) << 24);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -513,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         atomicExch(p.status, KVQ_ERR_TIMEOUT);
     };
     auto wait1 = [&](uint64_t *bar, int parity) {
-        return mbar_try_wait(bar, parity & 1) || wait_slow(bar, parity & 1, abort_flag, limit);
+        return mbar_wait_bounded(bar, parity & 1, abort_flag, limit);
     };
     // a wait of a whole warp: its lanes go on, or give up, together
     auto wait = [&](uint64_t *bar, int parity) {
@@ -528,13 +551,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         for (int j = 0; j < 2; j++) {
             mbar_init(&ctl->kfull[j], kConvWarps / 2);
             mbar_init(&ctl->vfull[j], kConvWarps / 2);
-            mbar_init(&ctl->sfull[j], 1);
-            mbar_init(&ctl->pfull[j], kSoftWarps);
-            mbar_init(&ctl->pvdone[j], 1);
+            for (int g = 0; g < 2; g++) {
+                mbar_init(&ctl->sfull[g][j], 1);
+                mbar_init(&ctl->pfull[g][j], kSoftWarps);
+                mbar_init(&ctl->pvdone[g][j], 1);
+            }
         }
         for (int j = 0; j < 4; j++) mbar_init(&ctl->par[j], kConvWarps);
         mbar_init(&ctl->qfull, kSoftWarps);
-        mbar_init(&ctl->soft, kSoftWarps);
+        mbar_init(&ctl->soft, 2 * kSoftWarps);
         mbar_init(&ctl->drain, 1);
         ctl->abort = 0;
         fence_mbar_init();
@@ -553,198 +578,42 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     const uint32_t tmem = ctl->tmem;
     const int n_units = w.n_units;
 
-    if (warp == kProducerWarp) {
-        // ====================== producer ======================
-        if (lane == 0 && n_units > 0) {
-            const uint64_t pol = l2_evict_first_policy();
-            const int kr = DH * p.k.bits / 8, vr = DH * p.v.bits / 8;
-            const bool ks = p.k.bits != 16 && p.fmt != KVQ_FMT_TENSOR, vs = p.v.bits != 16 && p.fmt != KVQ_FMT_TENSOR;
-            const int ksb = DH / p.k.group * scale_vals(p.fmt) * 2, vsb = DH / p.v.group * scale_vals(p.fmt) * 2;
-            Walk it;
-            it.start(p, w);
-            int e = 0, s = 0, use = 0;          // entries filled; the next one's place and use
-            for (int i = 0; i < n_units; i++) {
-                const int head = it.inner / it.s.rtn, t0 = it.tile * TT;
-                const int nv = min(TT, it.s.total - t0);
-                int64_t row;
-                if (p.rows.block_table != nullptr) {
-                    int page = p.rows.block_table[(int64_t)it.b * p.rows.max_pages + it.tile];
-                    page = min(max(page, 0), p.rows.n_pages - 1);   // stay inside the pool
-                    row = ((int64_t)page * p.rows.heads + head) * kPageTokens;
-                } else {
-                    row = ((int64_t)it.b * p.rows.heads + head) * p.rows.cap + t0;
-                }
-                const int nsc = (nv + 7) & ~7;      // rows whose scales are whole 16-byte pieces
-                bool ok = true;
-#pragma unroll 1
-                for (int kv = 0; kv < 2; kv++, e++) {
-                    if (use > 0 && !wait1(&ctl->empty[s], use - 1)) {
-                        give_up();
-                        ok = false;
-                        break;
-                    }
-                    const CacheTensor &t = kv ? p.v : p.k;
-                    const int rb = kv ? vr : kr, sb = kv ? vsb : ksb;
-                    const bool sc = kv ? vs : ks;
-                    uint8_t *dst = smem + (uint32_t)s * p.l.entry_bytes;
-                    mbar_arrive_expect_tx(&ctl->full[s], (uint32_t)(nv * rb + (sc ? nsc * sb : 0)));
-                    bulk_load_hint(dst, t.codes + row * rb, (uint32_t)(nv * rb), &ctl->full[s], pol);
-                    if (sc)
-                        bulk_load_hint(dst + p.l.off_scales, reinterpret_cast<const uint8_t *>(t.scales) + row * sb,
-                                       (uint32_t)(nsc * sb), &ctl->full[s], pol);
-                    if (++s == E) {
-                        s = 0;
-                        ++use;
-                    }
-                }
-                if (!ok) break;
-                it.next(p);
-            }
-            // copies in flight land before the CTA ends, whatever the other roles did
-            for (int k = e > E ? e - E : 0; k < e; k++) (void)mbar_wait_drain(&ctl->full[k % E], (k / E) & 1, limit);
-        }
-    } else if (warp == kMmaWarp) {
-        // ====================== MMA issuer ======================
-        if (lane == 0 && n_units > 0) {
-            const uint32_t sbase = smem_u32(smem);
-            const bool q2 = p.q_dtype == KVQ_F32;
-            Walk it;
-            it.start(p, w);
-            int seg = -1;
-            bool ok = true, first_prev = false;
-            auto issue_pv = [&](int i, bool first) -> bool {
-                const int j = i & 1, vb = i & (VB - 1);
-                if (!wait1(&ctl->vfull[vb], i >> (VB - 1))) return false;
-                if (!wait1(&ctl->pfull[j], i >> 1)) return false;
-                tc_fence_after();
-                const uint32_t v0 = sbase + p.l.off_v + (uint32_t)vb * p.l.v_bytes;
-#pragma unroll 1
-                for (int part = 0; part <= p.l.v_grouped; part++)
-#pragma unroll
-                    for (int kk = 0; kk < TT / 16; kk++)
-                        umma_f16_ts(tmem + COL_O, tmem + COL_S + 128u * j + 8u * kk,
-                                    sw128_mn_desc(v0 + part * p.l.lo + 2048u * kk, PANEL, 1024u), IDESC_O,
-                                    first && part == 0 && kk == 0 ? 0u : 1u);
-                umma_commit(&ctl->pvdone[j]);
-                return true;
-            };
-            auto issue_s = [&](int i) -> bool {
-                const int kb = i & (KB - 1);
-                if (!wait1(&ctl->kfull[kb], i >> (KB - 1))) return false;
-                tc_fence_after();
-                const uint32_t k0 = sbase + p.l.off_k + (uint32_t)kb * p.l.k_bytes;
-#pragma unroll 1
-                for (int part = 0; part <= p.l.k_grouped; part++)
-#pragma unroll 1
-                    for (int qp = 0; qp <= (q2 ? 1 : 0); qp++)
-#pragma unroll
-                        for (int kk = 0; kk < DH / 16; kk++)
-                            umma_f16_ts(tmem + COL_S + 128u * (i & 1), tmem + (qp ? COL_QLO : COL_Q) + 8u * kk,
-                                        sw128_desc(k0 + part * p.l.lo + (uint32_t)(kk >> 2) * PANEL + 32u * (kk & 3)),
-                                        IDESC_S, part == 0 && qp == 0 && kk == 0 ? 0u : 1u);
-                umma_commit(&ctl->sfull[i & 1]);
-                return true;
-            };
-            bool issued = false;
-            for (int i = 0; i <= n_units && ok; i++) {
-                const bool have = i < n_units;
-                const bool first = have && (i == 0 || it.tile == 0);
-                // a new segment's queries replace the old ones: its scores wait for the last P V
-                if (i > 0 && (first || !have)) ok = issue_pv(i - 1, first_prev);
-                if (ok && first) ok = wait1(&ctl->qfull, ++seg);
-                if (ok && have) {
-                    ok = issue_s(i);
-                    issued |= ok;
-                }
-                if (ok && i > 0 && have && !first) ok = issue_pv(i - 1, first_prev);
-                first_prev = first;
-                if (have) it.next(p);
-            }
-            if (!ok) give_up();
-            if (issued) {
-                umma_commit(&ctl->drain);
-                (void)mbar_wait_drain(&ctl->drain, 0, limit);
-            }
-        }
-    } else if (warp >= kConvWarp0) {
-        // ====================== converters ======================
-        // four warps turn K tiles, four V tiles
-        const int kv = warp >= kConvWarp0 + kConvWarps / 2;
-        const int ct = (threadIdx.x - 32 * kConvWarp0) & (kConvThreads - 1);
-        const CacheTensor &t = kv ? p.v : p.k;
-        const float tensor = p.fmt == KVQ_FMT_TENSOR ? __half2float(t.scales[0]) : 1.f;
-        const int bufs = kv ? VB : KB;
-        uint8_t *tiles = smem + (kv ? p.l.off_v : p.l.off_k);
-        const uint32_t tile_bytes = kv ? p.l.v_bytes : p.l.k_bytes;
-        uint64_t *ready = kv ? ctl->vfull : ctl->kfull, *used = kv ? ctl->pvdone : ctl->sfull;
-        Walk it;
-        if (n_units > 0) it.start(p, w);
-        bool ok = true;
-        int s = kv, use = 0;
-        for (int i = 0; i < n_units; i++) {
-            const int nv = min(TT, it.s.total - it.tile * TT);
-            ok = wait(&ctl->full[s], use);
-            // the operand's last use: S, or P V, of tile i - bufs
-            if (ok && i >= bufs) ok = wait(&used[(i - bufs) & 1], (i - bufs) >> 1);
-            if (!ok) break;
-            const uint8_t *entry = smem + (uint32_t)s * p.l.entry_bytes;
-            const int buf = i & (bufs - 1);
-            if (kv)
-                convert_any<DH, true>(p, entry, tiles + (uint32_t)buf * tile_bytes, nv, ct, tensor, par->lv[i & 3],
-                                      par->iv[i & 3]);
-            else
-                convert_any<DH, false>(p, entry, tiles + (uint32_t)buf * tile_bytes, nv, ct, tensor, par->sk[i & 3],
-                                       nullptr);
-            fence_proxy_async_shared();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&ctl->par[i & 3]);       // before the tile can be used, so that its
-                mbar_arrive(&ready[buf]);            // phase is over when the slot comes round
-                mbar_arrive(&ctl->empty[s]);
-            }
-            s += 2;
-            if (s >= E) {
-                s -= E;
-                ++use;
-            }
-            it.next(p);
-        }
-        if (!ok) give_up();
-    } else {
+    if (warp < 2 * kSoftWarps) {
+        more_regs<kSoftRegs>();
         // ====================== softmax ======================
-        const uint32_t lane_off = (uint32_t)(32 * warp) << 16;
-        const int place = 32 * warp + lane;          // TMEM lane
+        // two groups of four warps: group g takes tokens 64 g .. 64 g + 63 of every tile, with
+        // an O of its own; while one works on its P the tensor cores work for the other
+        const int grp = warp / kSoftWarps;
+        const int place = threadIdx.x & (TT - 1);    // TMEM lane
+        const uint32_t lane_off = (uint32_t)(place & ~31) << 16;
+        const uint32_t s_at = tmem + COL_S + 64u * grp + lane_off, o_at = tmem + COL_O + 128u * grp + lane_off;
         float *stage = reinterpret_cast<float *>(smem + p.l.off_stage);
         const float osign = p.fmt == KVQ_FMT_TENSOR && __half2float(p.v.scales[0]) < 0.f ? -1.f : 1.f;
-        Walk it;
-        if (n_units > 0) it.start(p, w);
         bool ok = true;
         int syncs = 0;
-        auto soft_sync = [&]() {                     // the four warps meet
+        auto soft_sync = [&]() {                     // the eight warps meet
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->soft);
-            const bool r = wait(&ctl->soft, syncs & 1);
-            ++syncs;
-            return r;
+            return wait(&ctl->soft, syncs++);
         };
         // What a thread keeps of its row; the next segment's is made while the last tile of the
         // current one is with the tensor cores.
         struct Row {
-            int rows, copies, tb;                    // rows of the tile, their copies; first token of this copy
+            int rows, copies, tb;                    // rows of the tile, their copies; first of the group's
+                                                     // tokens that this copy takes
             float rf;                                // factor of a score: tau log2(e), the query's power of two
             uint64_t mask;                           // drafted tokens that the row attends
         };
         // this thread's row of the walk's segment, its query into TMEM
         auto open = [&](const Walk &o) {
-            const int head = o.inner / o.s.rtn, rt = o.inner % o.s.rtn;
             Row x;
-            x.rows = min(kTreeRows, o.s.n * p.G - rt * kTreeRows);
+            x.rows = min(kTreeRows, o.s.n * p.G - o.rt * kTreeRows);
             x.copies = x.rows <= 32 ? 4 : x.rows <= 64 ? 2 : 1;
             const int r = place & (TT / x.copies - 1);
-            x.tb = place - r;
-            const int rr = rt * kTreeRows + r, qi = rr / p.G;
+            x.tb = (place - r) / 2;
+            const int rr = o.rt * kTreeRows + r, qi = rr / p.G;
             const bool live = r < x.rows;
-            const int64_t at = (((int64_t)o.b * p.n_tree + qi) * p.n_q_heads + (int64_t)head * p.G + rr % p.G) * DH;
+            const int64_t at = (((int64_t)o.b * p.n_tree + qi) * p.n_q_heads + (int64_t)o.head * p.G + rr - qi * p.G) * DH;
             x.rf = p.tau_log2e;
             x.mask = 0;
             if (live) {
@@ -760,51 +629,68 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 x.rf = p.tau_log2e * pow2i(ex);
                 return pow2i(-ex);
             };
-            if (p.q_dtype != KVQ_F32) {
-                uint4 u[DH / 8];
-                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + at);
+            if (p.q_dtype == KVQ_F16 && grp == 1) return x;
+            // 16 elements of the row from element d, as fp32
+            auto load16 = [&](int d, float (&e)[16]) {
+                if (!live) {
 #pragma unroll
-                for (int k = 0; k < DH / 8; k++) u[k] = live ? src[k] : make_uint4(0u, 0u, 0u, 0u);
-                uint32_t *h = reinterpret_cast<uint32_t *>(u);
-                if (p.q_dtype == KVQ_BF16) {
-                    float a = 0.f;
+                    for (int k = 0; k < 16; k++) e[k] = 0.f;
+                } else if (p.q_dtype == KVQ_F32) {
+                    const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + at + d);
 #pragma unroll
-                    for (int k = 0; k < DH / 2; k++)
-                        a = fmaxf(a, fmaxf(fabsf(__uint_as_float(h[k] << 16)), fabsf(__uint_as_float(h[k] & 0xffff0000u))));
-                    const float pre = level(a);
-#pragma unroll
-                    for (int k = 0; k < DH / 2; k++)
-                        h[k] = pack_half2(__uint_as_float(h[k] << 16) * pre, __uint_as_float(h[k] & 0xffff0000u) * pre);
-                }
-#pragma unroll
-                for (int k = 0; k < DH / 32; k++)
-                    tmem_st16(tmem + COL_Q + lane_off + 16u * k, *reinterpret_cast<uint32_t(*)[16]>(h + 16 * k));
-            } else {
-                const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + at);
-                const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
-                float a = 0.f;
-#pragma unroll 4
-                for (int k = 0; k < DH / 4; k++) {
-                    const float4 f = live ? src[k] : none;
-                    a = fmaxf(fmaxf(a, fmaxf(fabsf(f.x), fabsf(f.y))), fmaxf(fabsf(f.z), fabsf(f.w)));
-                }
-                const float pre = level(a);
-#pragma unroll 1
-                for (int c = 0; c < DH / 32; c++) {
-                    uint32_t hi[16], lo[16];
-#pragma unroll
-                    for (int k = 0; k < 8; k++) {
-                        float4 f = live ? src[8 * c + k] : none;
-                        f.x *= pre; f.y *= pre; f.z *= pre; f.w *= pre;
-                        hi[2 * k] = pack_half2(f.x, f.y);
-                        hi[2 * k + 1] = pack_half2(f.z, f.w);
-                        const float2 b0 = unpack_half2(hi[2 * k]), b1 = unpack_half2(hi[2 * k + 1]);
-                        lo[2 * k] = pack_half2(f.x - b0.x, f.y - b0.y);
-                        lo[2 * k + 1] = pack_half2(f.z - b1.x, f.w - b1.y);
+                    for (int k = 0; k < 4; k++) {
+                        const float4 f = src[k];
+                        e[4 * k] = f.x; e[4 * k + 1] = f.y; e[4 * k + 2] = f.z; e[4 * k + 3] = f.w;
                     }
-                    tmem_st16(tmem + COL_Q + lane_off + 16u * c, hi);
-                    tmem_st16(tmem + COL_QLO + lane_off + 16u * c, lo);
+                } else {
+                    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + at + d);
+#pragma unroll
+                    for (int k = 0; k < 2; k++) {
+                        const uint4 u = src[k];
+                        const uint32_t ww[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int y = 0; y < 4; y++) {
+                            const float2 h = unpack_half2(ww[y]);
+                            const bool half = p.q_dtype == KVQ_F16;
+                            e[8 * k + 2 * y] = half ? h.x : __uint_as_float(ww[y] << 16);
+                            e[8 * k + 2 * y + 1] = half ? h.y : __uint_as_float(ww[y] & 0xffff0000u);
+                        }
+                    }
                 }
+            };
+            if (live) {
+                // the row's lines, all at once: the loops below find them in L1
+                const char *src = static_cast<const char *>(p.q) + at * (p.q_dtype == KVQ_F32 ? 4 : 2);
+                const int bytes = DH * (p.q_dtype == KVQ_F32 ? 4 : 2);
+                for (int k = 0; k < bytes; k += 128) asm volatile("prefetch.global.L1 [%0];" ::"l"(src + k));
+            }
+            float pre = 1.f;
+            if (p.q_dtype != KVQ_F16) {
+                float a = 0.f;
+#pragma unroll 1
+                for (int d = 0; d < DH; d += 16) {
+                    float e[16];
+                    load16(d, e);
+#pragma unroll
+                    for (int k = 0; k < 16; k++) a = fmaxf(a, fabsf(e[k]));
+                }
+                pre = level(a);
+                if (grp == 1) return x;
+            }
+#pragma unroll 1
+            for (int d = 0; d < DH; d += 16) {
+                float e[16];
+                uint32_t hi[8], lo[8];
+                load16(d, e);
+#pragma unroll
+                for (int k = 0; k < 8; k++) {
+                    const float y0 = e[2 * k] * pre, y1 = e[2 * k + 1] * pre;
+                    hi[k] = pack_half2(y0, y1);
+                    const float2 b = unpack_half2(hi[k]);
+                    lo[k] = pack_half2(y0 - b.x, y1 - b.y);
+                }
+                tmem_st8(tmem + COL_Q + lane_off + d / 2, hi);
+                if (p.q_dtype == KVQ_F32) tmem_st8(tmem + COL_QLO + lane_off + d / 2, lo);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -812,164 +698,341 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             if (lane == 0) mbar_arrive(&ctl->qfull);
             return x;
         };
-        float m = -INFINITY, l = 0.f;
-        int seg0 = 0;                                // the segment's first unit in this CTA
-        Row row{}, next{};
-        if (n_units > 0) row = open(it);
-        for (int i = 0; i < n_units; i++) {
-            const int j = i & 1, t0 = it.tile * TT;
-            const int copies = row.copies, tb = row.tb;
-            const bool last = i == n_units - 1 || it.tile == it.s.tiles - 1;
-            Walk ahead = it;
-            ahead.next(p);
-
-            // ---- scores of the tile
-            ok = wait(&ctl->par[i & 3], i >> 2) &&
-                 wait(&ctl->sfull[j], i >> 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t s_at = tmem + COL_S + 128u * j + lane_off;
-            const float *sk = par->sk[i & 3] + tb, *lv = par->lv[i & 3] + tb, *iv = par->iv[i & 3] + tb;
-            const bool whole = t0 + TT <= it.s.len;
-            // one 32-token chunk at a time: its z, its maximum, its P over S's columns
-            const int chunks = 4 / copies;
-            const uint32_t p_at = s_at + (uint32_t)tb / 2;
+        Walk it;
+        Row row{};
+        int i = 0;                                   // units done
+        // segment by segment; a first pass without tiles only opens the first one
+        it.start(p, w);
+        bool opened = false;
 #pragma unroll 1
-            for (int c = 0; c < chunks; c++) {
-                uint32_t a[32], pw[16];
-                uint64_t z[16];
-                tmem_ld32(s_at + tb + 32u * c, a);
-                const uint32_t vis = whole ? FULL : visible(t0 + tb + 32 * c, it.s.len, row.mask);
-                const float mx = scores32(a, sk + 32 * c, lv + 32 * c, row.rf, vis, z);
-                const bool set = m == -INFINITY && mx > -INFINITY, up = !set && mx > m + kMoveAt;
-                float alpha = 1.f;
-                if (set || up) {
-                    const float to = floorf(mx) - kHead;
-                    if (up) alpha = ex2(m - to);             // m and to are whole: a power of two
-                    m = to;
-                    l *= alpha;
-                }
-                if (__any_sync(FULL, up)) {
+        while (it.count) {
+            float m = -INFINITY, l = 0.f;
+            const int i0 = i, copies = row.copies, tb = row.tb, count = opened ? it.count : 0;
+#pragma unroll 1
+            for (int k = 0; k < count; k++, i++) {
+                // ---- P of this thread's tokens, over the columns of their scores
+                const int j = i & 1;
+                ok = wait(&ctl->par[i & 3], i >> 2) && wait(&ctl->sfull[grp][j], i >> 1);
+                if (!ok) break;
+                tc_fence_after();
+                const int at = HT * grp + tb;
+                const float *sk = par->sk[i & 3] + at, *lv = par->lv[i & 3] + at, *iv = par->iv[i & 3] + at;
+                const int t0 = (it.tile + k) * TT + HT * grp;
+                const bool whole = t0 + HT <= it.s.len;
+                const uint32_t p_at = s_at + (uint32_t)tb / 2;
+                // raise m to fit a maximum; false: a wait gave up
+                auto fit = [&](float mx, int c) -> bool {
+                    const bool set = m == -INFINITY && mx > -INFINITY, up = !set && mx > m + kMoveAt;
+                    float alpha = 1.f;
+                    if (set || up) {
+                        const float to = floorf(mx) - kHead;
+                        if (up) alpha = ex2(m - to);             // m and to are whole: a power of two
+                        m = to;
+                        l *= alpha;
+                    }
+                    if (!__any_sync(FULL, up)) return true;
                     // m moved too far for some row: O follows (every P V before this tile is in
                     // it; in a segment's first tile there is nothing yet), and this tile's P
-                    if (i > seg0) {
-                        if (!(ok = wait(&ctl->pvdone[j ^ 1], (i - 1) >> 1))) break;
+                    uint32_t x[16];
+                    if (k > 0) {
+                        if (!wait(&ctl->pvdone[grp][j ^ 1], (i - 1) >> 1)) return false;
                         tc_fence_after();
 #pragma unroll 1
-                        for (int x = 0; x < DH / 32; x++) {
-                            tmem_ld32(tmem + COL_O + lane_off + 32u * x, a);
+                        for (int q = 0; q < DH / 16; q++) {
+                            tmem_ld16(o_at + 16u * q, x);
 #pragma unroll
-                            for (int y = 0; y < 32; y++) a[y] = __float_as_uint(__uint_as_float(a[y]) * alpha);
-                            tmem_st32(tmem + COL_O + lane_off + 32u * x, a);
+                            for (int y = 0; y < 16; y++) x[y] = __float_as_uint(__uint_as_float(x[y]) * alpha);
+                            tmem_st16(o_at + 16u * q, x);
                         }
                     }
                     const uint32_t alpha2 = pack_half2(alpha, alpha);
 #pragma unroll 1
-                    for (int x = 0; x < c; x++) {
+                    for (int n = 0; n < c; n++) {
+                        uint32_t y[8];
                         tmem_st_wait();
-                        tmem_ld16(p_at + 16u * x, pw);
+                        tmem_ld8(p_at + 8u * n, y);
 #pragma unroll
-                        for (int y = 0; y < 16; y++) pw[y] = hmul2_u32(pw[y], alpha2);
-                        tmem_st16(p_at + 16u * x, pw);
+                        for (int q = 0; q < 8; q++) y[q] = hmul2_u32(y[q], alpha2);
+                        tmem_st8(p_at + 8u * n, y);
                     }
-                }
-                l += probs32(z, iv + 32 * c, m == -INFINITY ? 0.f : m, pw);
-                tmem_st16(p_at + 16u * c, pw);
-            }
-            if (!ok) break;
-            if (copies > 1) {
-                // the other copies' tokens
-                uint32_t none[16];
-#pragma unroll
-                for (int x = 0; x < 16; x++) none[x] = 0u;
-#pragma unroll 1
-                for (int c = chunks; c < 4; c++) tmem_st16(s_at + (((uint32_t)tb / 2 + 16u * c) & 63u), none);
-            }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl->pfull[j]);
-            // every score of the segment is done: the next one's queries may come in
-            if (last && i + 1 < n_units) next = open(ahead);
-
-            // ---- the segment's last tile: join the copies, write the output or a partial
-            if (last) {
-                const int head = it.inner / it.s.rtn, rt = it.inner % it.s.rtn;
-                const int nr = TT / copies, r = place - tb, rows = row.rows;
-                float M = m, L = l;
-                if (copies > 1) {
-                    ctl->ml[place] = make_float2(m, l);
-                    if (!(ok = soft_sync())) break;
-                    M = -INFINITY;
-                    L = 0.f;
-                    for (int c = 0; c < copies; c++) M = fmaxf(M, ctl->ml[c * nr + r].x);
-                    for (int c = 0; c < copies; c++) {
-                        const float2 x = ctl->ml[c * nr + r];
-                        L += x.x == -INFINITY ? 0.f : x.y * ex2(x.x - M);
-                    }
-                }
-                float f = m == -INFINITY ? 0.f : ex2(m - M) * osign;
-                const long long u0 = w.u0 + i - it.tile;
-                const int ca = range_cta(u0, w.n, w.p), cb = range_cta(u0 + it.s.tiles - 1, w.n, w.p);
-                const bool direct = ca == cb;
-                // a CTA leaves two partials at most: of its first segment, and of its last
-                const int slot = 2 * (int)blockIdx.x + (i - it.tile <= 0 ? 0 : 1);
-                float *part = p.slots + (int64_t)slot * tree_slot_floats(p.slot_rows, DH);
-                if (direct) f = L != 0.f ? f / L : 0.f;
-                if (place == 0 && ca == (int)blockIdx.x)
-                    p.seg[((int64_t)it.b * p.rows.heads + head) * p.row_tiles + rt] = make_int4(slot, ca, cb - ca + 1, 0);
-                if (!direct && place < rows)
-                    *reinterpret_cast<float2 *>(part + (int64_t)p.slot_rows * DH + 2 * place) = make_float2(M, L);
-                // columns col .. col + 3 of a row of the tile
-                auto put = [&](int rr, int col, const float (&y)[4]) {
-                    if (!direct) {
-                        *reinterpret_cast<float4 *>(part + (int64_t)rr * DH + col) = make_float4(y[0], y[1], y[2], y[3]);
-                        return;
-                    }
-                    rr += rt * kTreeRows;
-                    store4(p.out, (((int64_t)it.b * p.n_tree + rr / p.G) * p.n_q_heads + (int64_t)head * p.G + rr % p.G) * DH + col,
-                           p.out_dtype, y);
+                    return true;
                 };
-                if (!(ok = wait(&ctl->pvdone[j], i >> 1))) break;
-                tc_fence_after();
+                // 16 tokens at a time; the next ones' scores are on their way meanwhile
+                const int chunks = 4 / copies;
+                uint32_t a[16];
+                tmem_ld16_async(s_at + tb, a);
 #pragma unroll 1
-                for (int c = 0; c < DH / 32; c++) {
-                    uint32_t o[32];
-                    tmem_ld32(tmem + COL_O + lane_off + 32u * c, o);
-                    if (copies == 1) {
-                        if (place < rows)
-#pragma unroll
-                            for (int x = 0; x < 32; x += 4) {
-                                float y[4];
-#pragma unroll
-                                for (int d = 0; d < 4; d++) y[d] = f == 0.f ? 0.f : __uint_as_float(o[x + d]) * f;
-                                put(place, 32 * c + x, y);
-                            }
-                        continue;
-                    }
-                    if (c > 0 && !(ok = soft_sync())) break;         // the staging was read
-#pragma unroll
-                    for (int x = 0; x < 32; x++) stage[place * STAGE_LD + x] = f == 0.f ? 0.f : __uint_as_float(o[x]) * f;
-                    if (!(ok = soft_sync())) break;
-#pragma unroll 1
-                    for (int x = place; x < rows * 8; x += TT) {
-                        const int rr = x >> 3, col = (x & 7) * 4;
-                        float y[4] = {0.f, 0.f, 0.f, 0.f};
-                        for (int k = 0; k < copies; k++)
-#pragma unroll
-                            for (int d = 0; d < 4; d++) y[d] += stage[(k * nr + rr) * STAGE_LD + col + d];
-                        put(rr, 32 * c + col, y);
-                    }
+                for (int c = 0; c < chunks; c++) {
+                    uint32_t pw[8];
+                    uint64_t z[8];
+                    tmem_ld16_wait(a);
+                    const uint32_t vis = whole ? FULL : visible(t0 + tb + 16 * c, it.s.len, row.mask) | 0xffff0000u;
+                    const float mx = scores<16>(a, sk + 16 * c, lv + 16 * c, row.rf, vis, z);
+                    if (c + 1 < chunks) tmem_ld16_async(s_at + tb + 16u * (c + 1), a);
+                    if (!(ok = fit(mx, c))) break;
+                    l += probs<16>(z, iv + 16 * c, m == -INFINITY ? 0.f : m, pw);
+                    // (columns of scores that are already read: P takes half as many)
+                    tmem_st8(p_at + 8u * c, pw);
                 }
                 if (!ok) break;
-                row = next;
-                m = -INFINITY;
-                l = 0.f;
-                seg0 = i + 1;
+                if (copies > 1) {
+                    // the other copies' tokens
+                    uint32_t none[8];
+#pragma unroll
+                    for (int x = 0; x < 8; x++) none[x] = 0u;
+#pragma unroll 1
+                    for (int c = chunks; c < 4; c++) tmem_st8(s_at + (((uint32_t)tb / 2 + 8u * c) & 31u), none);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->pfull[grp][j]);
             }
+            if (!ok) break;
+            // ---- the next segment's queries come in once both groups' scores are done
+            const int last = i - 1;
+            Walk ahead = it;
+            if (opened) {
+                ahead.next(p);
+                if (ahead.count && grp == 0) {
+                    if (!(ok = wait(&ctl->sfull[1][last & 1], last >> 1))) break;
+                    tc_fence_after();
+                }
+            }
+            Row next{};
+            if (ahead.count) next = open(ahead);
+            if (!opened) {
+                opened = true;
+                row = next;
+                continue;
+            }
+            // join the groups and copies of every row; the output, or a partial
+            const int nr = TT / copies, r = place & (nr - 1), rows = row.rows;
+            ctl->ml[grp][place] = make_float2(m, l);
+            if (!(ok = soft_sync())) break;
+            float M = -INFINITY, L = 0.f;
+#pragma unroll 1
+            for (int c = r; c < 2 * TT; c += nr) M = fmaxf(M, ctl->ml[0][c].x);
+#pragma unroll 1
+            for (int c = r; c < 2 * TT; c += nr) {
+                const float2 x = ctl->ml[0][c];
+                L += x.x == -INFINITY ? 0.f : x.y * ex2(x.x - M);
+            }
+            const long long u0 = w.u0 + i0 - it.tile, u1 = u0 + it.s.tiles;
+            const bool opens = u0 >= w.u0, direct = opens && u1 <= w.u0 + n_units;
+            // a CTA leaves two partials at most: of its first segment, and of its last
+            const int slot = 2 * (int)blockIdx.x + (i0 == 0 ? 0 : 1);
+            float *part = p.slots + (int64_t)slot * tree_slot_floats(p.slot_rows, DH);
+            float f = m == -INFINITY ? 0.f : ex2(m - M) * osign;
+            if (direct) f = L != 0.f ? f / L : 0.f;
+            if (threadIdx.x == 0 && opens)
+                p.seg[((int64_t)it.b * p.rows.heads + it.head) * p.row_tiles + it.rt] =
+                    make_int4(slot, blockIdx.x, direct ? 1 : range_cta(u1 - 1, w.n, w.p) - (int)blockIdx.x + 1, 0);
+            if (!direct && threadIdx.x < rows)
+                *reinterpret_cast<float2 *>(part + (int64_t)p.slot_rows * DH + 2 * place) = make_float2(M, L);
+            if (!(ok = wait(&ctl->pvdone[grp][last & 1], last >> 1))) break;
+            tc_fence_after();
+            // four columns of a row a thread: rows threadIdx.x / 4 and, of more than 64, + 64
+            const int r0 = threadIdx.x >> 2, col = (threadIdx.x & 3) * 4;
+            const int64_t out0 = ((int64_t)it.b * p.n_tree * p.n_q_heads + (int64_t)it.head * p.G) * DH + col;
+#pragma unroll 1
+            for (int c = 0; c < DH / 16; c++) {
+                uint32_t o[16];
+                tmem_ld16(o_at + 16u * c, o);
+                if (c > 0 && !(ok = soft_sync())) break;             // the staging was read
+#pragma unroll
+                for (int x = 0; x < 16; x++)
+                    stage[(grp * TT + place) * STAGE_LD + x] = f == 0.f ? 0.f : __uint_as_float(o[x]) * f;
+                if (!(ok = soft_sync())) break;
+#pragma unroll 1
+                for (int k = 0; k < 2; k++) {
+                    const int rr = r0 + 64 * k;
+                    if (rr >= rows) break;
+                    float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                    for (int q = rr; q < 2 * TT; q += nr)
+#pragma unroll
+                        for (int d = 0; d < 4; d++) y[d] += stage[q * STAGE_LD + col + d];
+                    const int gr = it.rt * kTreeRows + rr, qi = gr / p.G;
+                    if (direct)
+                        store4(p.out, out0 + ((int64_t)qi * (p.n_q_heads - p.G) + gr) * DH + 16 * c, p.out_dtype, y);
+                    else
+                        *reinterpret_cast<float4 *>(part + rr * DH + col + 16 * c) = make_float4(y[0], y[1], y[2], y[3]);
+                }
+            }
+            if (!ok) break;
+            row = next;
             it = ahead;
         }
         if (!ok) give_up();
+    } else if (warp >= kConvWarp0) {
+        fewer_regs<kConvRegs>();
+        // ====================== converters ======================
+        // four warps turn K tiles, four V tiles
+        const int kv = warp >= kConvWarp0 + kConvWarps / 2;
+        const int ct = (threadIdx.x - 32 * kConvWarp0) & (kConvThreads - 1);
+        const CacheTensor &t = kv ? p.v : p.k;
+        const float tensor = p.fmt == KVQ_FMT_TENSOR ? __half2float(t.scales[0]) : 1.f;
+        const int bufs = kv ? VB : KB;
+        uint8_t *tiles = smem + (kv ? p.l.off_v : p.l.off_k);
+        const uint32_t tile_bytes = kv ? p.l.v_bytes : p.l.k_bytes;
+        uint64_t *ready = kv ? ctl->vfull : ctl->kfull, *used = kv ? ctl->pvdone[1] : ctl->sfull[1];
+        bool ok = true;
+        int s = kv, use = 0, i = 0;
+        Walk it;
+#pragma unroll 1
+        for (it.start(p, w); it.count && ok; it.next(p)) {
+#pragma unroll 1
+            for (int k = 0; k < it.count; k++, i++) {
+                const int nv = min(TT, it.s.total - (it.tile + k) * TT);
+                ok = wait(&ctl->full[s], use);
+                // the operand's last use: S, or P V, of tile i - bufs
+                if (ok && i >= bufs) ok = wait(&used[(i - bufs) & 1], (i - bufs) >> 1);
+                if (!ok) break;
+                const uint8_t *entry = smem + (uint32_t)s * p.l.entry_bytes;
+                const int buf = i & (bufs - 1);
+                if (kv)
+                    convert_any<DH, true>(p, entry, tiles + (uint32_t)buf * tile_bytes, nv, ct, tensor, par->lv[i & 3],
+                                          par->iv[i & 3]);
+                else
+                    convert_any<DH, false>(p, entry, tiles + (uint32_t)buf * tile_bytes, nv, ct, tensor, par->sk[i & 3],
+                                           nullptr);
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&ctl->par[i & 3]);       // before the tile can be used, so that its
+                    mbar_arrive(&ready[buf]);            // phase is over when the slot comes round
+                    mbar_arrive(&ctl->empty[s]);
+                }
+                s += 2;
+                if (s >= E) {
+                    s -= E;
+                    ++use;
+                }
+            }
+        }
+        if (!ok) give_up();
+    } else {
+        fewer_regs<kIssueRegs>();
+        if (warp == kProducerWarp && lane == 0) {
+            // ====================== producer ======================
+            const uint64_t pol = l2_evict_first_policy();
+            const int kr = DH * p.k.bits / 8, vr = DH * p.v.bits / 8;
+            const bool sc = p.fmt != KVQ_FMT_TENSOR;
+            const int ksb = sc && p.k.bits != 16 ? DH / p.k.group * scale_vals(p.fmt) * 2 : 0;   // 0: no scales
+            const int vsb = sc && p.v.bits != 16 ? DH / p.v.group * scale_vals(p.fmt) * 2 : 0;
+            int e = 0, s = 0, use = 0;          // entries filled; the next one's place and use
+            bool ok = true;
+            Walk it;
+#pragma unroll 1
+            for (it.start(p, w); it.count && ok; it.next(p)) {
+#pragma unroll 1
+                for (int t = it.tile; t < it.tile + it.count && ok; t++) {
+                    const int nv = min(TT, it.s.total - t * TT);
+                    int64_t row;
+                    if (p.rows.block_table != nullptr) {
+                        int page = p.rows.block_table[(int64_t)it.b * p.rows.max_pages + t];
+                        page = min(max(page, 0), p.rows.n_pages - 1);   // stay inside the pool
+                        row = ((int64_t)page * p.rows.heads + it.head) * kPageTokens;
+                    } else {
+                        row = ((int64_t)it.b * p.rows.heads + it.head) * p.rows.cap + t * TT;
+                    }
+                    const int nsc = (nv + 7) & ~7;      // rows whose scales are whole 16-byte pieces
+#pragma unroll 1
+                    for (int kv = 0; kv < 2; kv++, e++) {
+                        if (use > 0 && !(ok = wait1(&ctl->empty[s], use - 1))) break;
+                        const CacheTensor &ten = kv ? p.v : p.k;
+                        const int rb = kv ? vr : kr, sb = kv ? vsb : ksb;
+                        uint8_t *dst = smem + (uint32_t)s * p.l.entry_bytes;
+                        mbar_arrive_expect_tx(&ctl->full[s], (uint32_t)(nv * rb + nsc * sb));
+                        bulk_load_hint(dst, ten.codes + row * rb, (uint32_t)(nv * rb), &ctl->full[s], pol);
+                        if (sb)
+                            bulk_load_hint(dst + p.l.off_scales, reinterpret_cast<const uint8_t *>(ten.scales) + row * sb,
+                                           (uint32_t)(nsc * sb), &ctl->full[s], pol);
+                        if (++s == E) {
+                            s = 0;
+                            ++use;
+                        }
+                    }
+                }
+            }
+            if (!ok) give_up();
+            // copies in flight land before the CTA ends, whatever the other roles did
+#pragma unroll 1
+            for (int k = e > E ? e - E : 0; k < e; k++) (void)mbar_wait_drain(&ctl->full[k % E], (k / E) & 1, limit);
+        } else if (warp == kMmaWarp && n_units > 0) {
+            // ====================== MMA issuer ======================
+            // The whole warp walks, so that every operand is the same for all its lanes and stays
+            // in uniform registers; one lane issues.
+            const bool leader = elect_one();
+            const uint32_t tm = __shfl_sync(FULL, tmem, 0);
+            const uint32_t sbase = smem_u32(smem);
+            const uint64_t k_desc = sw128_desc(sbase + p.l.off_k), v_desc = sw128_mn_desc(sbase + p.l.off_v, PANEL, 1024u);
+            const uint32_t lo = p.l.lo >> 4;          // descriptors count 16-byte units
+            const int q_parts = p.q_dtype == KVQ_F32 ? 2 : 1;
+            // scores of tile i for group g's half of its tokens
+            auto issue_s = [&](int i, int g) {
+                const int kb = i & (KB - 1);
+                if (!wait(&ctl->kfull[kb], i >> (KB - 1))) return false;
+                tc_fence_after();
+#pragma unroll 1
+                for (int part = 0; part < (1 + p.l.k_grouped) * q_parts; part++) {
+                    const int kp = q_parts == 2 ? part >> 1 : part, qp = q_parts == 2 ? part & 1 : 0;
+                    const uint64_t d = k_desc + (kb * (p.l.k_bytes >> 4) + kp * lo + g * (HT * 128u >> 4));
+                    const uint32_t qa = tm + (qp ? COL_QLO : COL_Q), st = tm + COL_S + 64u * g;
+                    if (leader)
+#pragma unroll
+                        for (int kk = 0; kk < DH / 16; kk++)
+                            umma_f16_ts(st, qa + 8u * kk, d + ((kk >> 2) * (PANEL >> 4) + 2u * (kk & 3)), IDESC_S,
+                                        kk > 0 ? 1u : (uint32_t)(part > 0));
+                }
+                if (leader) umma_commit(&ctl->sfull[g][i & 1]);
+                __syncwarp();
+                return true;
+            };
+            // O += P V of tile i
+            auto issue_pv = [&](int i, int g, bool first) {
+                const int vb = i & (VB - 1);
+                if (!wait(&ctl->vfull[vb], i >> (VB - 1)) || !wait(&ctl->pfull[g][i & 1], i >> 1)) return false;
+                tc_fence_after();
+#pragma unroll 1
+                for (int part = 0; part <= p.l.v_grouped; part++) {
+                    const uint64_t d = v_desc + (vb * (p.l.v_bytes >> 4) + part * lo + g * (HT * 128u >> 4));
+                    const uint32_t ot = tm + COL_O + 128u * g, pa = tm + COL_S + 64u * g;
+                    if (leader)
+#pragma unroll
+                        for (int kk = 0; kk < HT / 16; kk++)
+                            umma_f16_ts(ot, pa + 8u * kk, d + 128u * kk, IDESC_O,
+                                        kk > 0 ? 1u : (uint32_t)(!first || part > 0));
+                }
+                if (leader) umma_commit(&ctl->pvdone[g][i & 1]);
+                __syncwarp();
+                return true;
+            };
+            int i = 0, seg = 0;
+            bool ok = true;
+            Walk it;
+#pragma unroll 1
+            for (it.start(p, w); it.count && ok; it.next(p)) {
+                const int count = __shfl_sync(FULL, it.count, 0);
+                // a new segment's queries replace the old ones: its scores wait for them
+                ok = wait(&ctl->qfull, seg++) && issue_s(i, 0) && issue_s(i, 1);
+                // a group's scores of the next tile follow its P V of this one (they share columns)
+#pragma unroll 1
+                for (int k = 0; k < count && ok; k++, i++) {
+                    const bool more = k + 1 < count;
+#pragma unroll 1
+                    for (int g = 0; g < 2 && ok; g++) ok = issue_pv(i, g, k == 0) && (!more || issue_s(i + 1, g));
+                }
+            }
+            if (!ok) give_up();
+            // every product issued completes before the CTA gives up its memory
+            if (leader) {
+                umma_commit(&ctl->drain);
+                (void)mbar_wait_drain(&ctl->drain, 0, limit);
+            }
+            __syncwarp();
+        }
     }
 
     tc_fence_before();
@@ -1004,7 +1067,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
     float L = 0.f, y[PER];
 #pragma unroll
     for (int d = 0; d < PER; d++) y[d] = 0.f;
-#pragma unroll 4
+#pragma unroll 2
     for (int k = 0; k < seg.z; k++) {
         const float *x = slot(k);
         const float2 ml = *reinterpret_cast<const float2 *>(x + (int64_t)p.slot_rows * DH + 2 * r);
@@ -1082,7 +1145,7 @@ bool plan_tree(const TreeParams &p, int max_smem, TreeLaunch *l)
     l->off_scales = std::max(kr, vr);
     const uint32_t ks = p.k.bits == 16 ? 0 : TT * (dh / p.k.group) * pair, vs = p.v.bits == 16 ? 0 : TT * (dh / p.v.group) * pair;
     l->entry_bytes = align_up(l->off_scales + std::max(ks, vs), 128);
-    const uint32_t fixed = 1024 + TT * STAGE_LD * 4 + (uint32_t)sizeof(Par) + (uint32_t)sizeof(Ctl) + 512;
+    const uint32_t fixed = 1024 + STAGE_BYTES + (uint32_t)sizeof(Par) + (uint32_t)sizeof(Ctl) + 512;
     // two converted tiles of K and of V where that leaves room for four raw ones
     for (int bufs = 2; bufs >= 1; bufs--) {
         l->k_bufs = bufs;
@@ -1096,7 +1159,7 @@ bool plan_tree(const TreeParams &p, int max_smem, TreeLaunch *l)
         l->off_k = align_up((uint32_t)l->entries * l->entry_bytes, 1024);
         l->off_v = l->off_k + bufs * l->k_bytes;
         l->off_stage = l->off_v + bufs * l->v_bytes;
-        l->off_par = align_up(l->off_stage + TT * STAGE_LD * 4, 16);
+        l->off_par = align_up(l->off_stage + STAGE_BYTES, 16);
         l->off_ctl = align_up(l->off_par + (uint32_t)sizeof(Par), 16);
         l->smem_bytes = l->off_ctl + sizeof(Ctl) + 1024;
         return l->smem_bytes <= (size_t)max_smem;
