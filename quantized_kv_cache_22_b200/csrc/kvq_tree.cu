@@ -101,6 +101,16 @@ __device__ __forceinline__ float lg2(float x)
 }
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
+__device__ __forceinline__ bool wait_bounded(uint64_t *bar, int parity, int *abort_flag, uint64_t limit)
+{
+    return mbar_wait_bounded(bar, parity & 1, abort_flag, limit);
+}
+// a wait of a whole warp: its lanes go on, or give up, together
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, int parity, int *abort_flag, uint64_t limit)
+{
+    return __all_sync(FULL, wait_bounded(bar, parity, abort_flag, limit)) != 0;
+}
+
 // ------------------------------------------------------------------ work split
 struct Seq {
     int len, n, total, tiles, rtn;      // cached, drafted, attended tokens; tiles; row tiles
@@ -395,7 +405,7 @@ __device__ __forceinline__ void convert(const uint8_t *raw, const uint16_t *sc, 
     if (CHECK && c == 0)
 #pragma unroll 1
         for (int u = 0; u < PASSES; u++) params(u * RPP + tr, (bad_rows >> u) & 1u);
-    if (ISV && nvalid < TT) {
+    if (__builtin_expect(ISV && nvalid < TT, 0)) {
         // the last tile: zeros past the sequence's end
         const uint4 none = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 1
@@ -409,30 +419,69 @@ __device__ __forceinline__ void convert(const uint8_t *raw, const uint16_t *sc, 
     }
 }
 
-template <int DH, bool ISV>
-__device__ __forceinline__ void convert_any(const TreeParams &p, const uint8_t *entry, uint8_t *dst, int nvalid, int ct,
-                                            float tensor, float *p0, float *p1)
+// The converter role: every tile of K (ISV false) or V that is the CTA's, one kind of code per
+// instance of the loop (a branch to the kind's code inside it would cost an instruction-cache
+// miss on every tile: 2.1 against 1.5 thousand cycles a tile, INT8).
+template <int DH, int KIND, bool GRP, bool ISV>
+__device__ __forceinline__ bool convert_tiles(const TreeParams &p, const Work &w, uint8_t *smem, Ctl *ctl, Par *par,
+                                              int ct, int *abort_flag, uint64_t limit)
 {
-    const CacheTensor &t = ISV ? p.v : p.k;
-    const bool grp = ISV ? p.l.v_grouped : p.l.k_grouped;
-    const int ng = DH / t.group, gshift = t.group == 32 ? 5 : t.group == 64 ? 6 : 7;
-    const uint16_t *sc = reinterpret_cast<const uint16_t *>(entry + p.l.off_scales);
-    const bool pt = p.fmt == KVQ_FMT_TENSOR;
-#define KVQ_CONVERT(KIND)                                                                                          \
-    if (grp)                                                                                                       \
-        convert<DH, KIND, true, ISV>(entry, sc, dst, p.l.lo, nvalid, ct, ng, gshift, tensor, pt, p0, p1);            \
-    else                                                                                                           \
-        convert<DH, KIND, false, ISV>(entry, sc, dst, p.l.lo, nvalid, ct, ng, gshift, tensor, pt, p0, p1);
-    switch (kind_of(t.bits, p.fmt)) {
-    case K_INT8: KVQ_CONVERT(K_INT8) break;
-    case K_INT4: KVQ_CONVERT(K_INT4) break;
-    case K_E4M3: KVQ_CONVERT(K_E4M3) break;
-    case K_ASYM: KVQ_CONVERT(K_ASYM) break;
-    default:
-        convert<DH, K_F16, false, ISV>(entry, sc, dst, p.l.lo, nvalid, ct, ng, gshift, tensor, pt, p0, p1);
-        break;
+    const CacheTensor &ten = ISV ? p.v : p.k;
+    const int ng = DH / ten.group, gshift = ten.group == 32 ? 5 : ten.group == 64 ? 6 : 7;
+    const bool is_tensor = p.fmt == KVQ_FMT_TENSOR;
+    const float tensor = is_tensor ? __half2float(ten.scales[0]) : 1.f;
+    const int bufs = ISV ? p.l.v_bufs : p.l.k_bufs, E = p.l.entries;
+    uint8_t *tiles = smem + (ISV ? p.l.off_v : p.l.off_k);
+    const uint32_t tile_bytes = ISV ? p.l.v_bytes : p.l.k_bytes;
+    uint64_t *ready = ISV ? ctl->vfull : ctl->kfull, *used = ISV ? ctl->pvdone[1] : ctl->sfull[1];
+    int s = ISV, use = 0, i = 0;
+    Walk it;
+#pragma unroll 1
+    for (it.start(p, w); it.count; it.next(p)) {
+        int left = it.s.total - it.tile * TT;
+#pragma unroll 1
+        for (int k = it.count; k > 0; k--, i++, left -= TT) {
+            if (!wait_warp(&ctl->full[s], use, abort_flag, limit)) return false;
+            // the operand's last use: S, or P V, of tile i - bufs
+            if (i >= bufs && !wait_warp(&used[(i - bufs) & 1], (i - bufs) >> 1, abort_flag, limit)) return false;
+            const uint8_t *entry = smem + (uint32_t)s * p.l.entry_bytes;
+            const int buf = i & (bufs - 1);
+            convert<DH, KIND, GRP, ISV>(entry, reinterpret_cast<const uint16_t *>(entry + p.l.off_scales),
+                                        tiles + (uint32_t)buf * tile_bytes, p.l.lo, min(TT, left), ct, ng, gshift, tensor,
+                                        is_tensor, ISV ? par->lv[i & 3] : par->sk[i & 3], par->iv[i & 3]);
+            fence_proxy_async_shared();
+            __syncwarp();
+            if ((ct & 31) == 0) {
+                mbar_arrive(&ctl->par[i & 3]);       // before the tile can be used, so that its
+                mbar_arrive(&ready[buf]);            // phase is over when the slot comes round
+                mbar_arrive(&ctl->empty[s]);
+            }
+            s += 2;
+            if (s >= E) {
+                s -= E;
+                ++use;
+            }
+        }
     }
-#undef KVQ_CONVERT
+    return true;
+}
+
+template <int DH, bool ISV>
+__device__ __forceinline__ bool convert_role(const TreeParams &p, const Work &w, uint8_t *smem, Ctl *ctl, Par *par,
+                                             int ct, int *abort_flag, uint64_t limit)
+{
+    const bool grp = ISV ? p.l.v_grouped : p.l.k_grouped;
+    switch (kind_of(ISV ? p.v.bits : p.k.bits, p.fmt) * 2 + grp) {
+    case 2 * K_INT8: return convert_tiles<DH, K_INT8, false, ISV>(p, w, smem, ctl, par, ct, abort_flag, limit);
+    case 2 * K_INT8 + 1: return convert_tiles<DH, K_INT8, true, ISV>(p, w, smem, ctl, par, ct, abort_flag, limit);
+    case 2 * K_INT4: return convert_tiles<DH, K_INT4, false, ISV>(p, w, smem, ctl, par, ct, abort_flag, limit);
+    case 2 * K_INT4 + 1: return convert_tiles<DH, K_INT4, true, ISV>(p, w, smem, ctl, par, ct, abort_flag, limit);
+    case 2 * K_E4M3: return convert_tiles<DH, K_E4M3, false, ISV>(p, w, smem, ctl, par, ct, abort_flag, limit);
+    case 2 * K_E4M3 + 1: return convert_tiles<DH, K_E4M3, true, ISV>(p, w, smem, ctl, par, ct, abort_flag, limit);
+    case 2 * K_ASYM: return convert_tiles<DH, K_ASYM, false, ISV>(p, w, smem, ctl, par, ct, abort_flag, limit);
+    case 2 * K_ASYM + 1: return convert_tiles<DH, K_ASYM, true, ISV>(p, w, smem, ctl, par, ct, abort_flag, limit);
+    default: return convert_tiles<DH, K_F16, false, ISV>(p, w, smem, ctl, par, ct, abort_flag, limit);
+    }
 }
 
 // ------------------------------------------------------------------ softmax
@@ -483,7 +532,7 @@ __device__ __forceinline__ float scores(const uint32_t (&a)[N], const float *sk,
         z[t] = fma2(mul2(pair(a[2 * t], a[2 * t + 1]), k.x), rf2, v.x);
         z[t + 1] = fma2(mul2(pair(a[2 * t + 2], a[2 * t + 3]), k.y), rf2, v.y);
     }
-    if (vis != FULL) {
+    if (__builtin_expect(vis != FULL, 0)) {
 #pragma unroll
         for (int t = 0; t < N / 2; t++)
             z[t] = pair((vis >> (2 * t)) & 1u ? first(z[t]) : -INFINITY,
@@ -535,13 +584,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         *static_cast<volatile int *>(abort_flag) = 1;
         atomicExch(p.status, KVQ_ERR_TIMEOUT);
     };
-    auto wait1 = [&](uint64_t *bar, int parity) {
-        return mbar_wait_bounded(bar, parity & 1, abort_flag, limit);
-    };
-    // a wait of a whole warp: its lanes go on, or give up, together
-    auto wait = [&](uint64_t *bar, int parity) {
-        return __all_sync(FULL, wait1(bar, parity)) != 0;
-    };
+    auto wait1 = [&](uint64_t *bar, int parity) { return wait_bounded(bar, parity, abort_flag, limit); };
+    auto wait = [&](uint64_t *bar, int parity) { return wait_warp(bar, parity, abort_flag, limit); };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < E; s++) {
@@ -730,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                         m = to;
                         l *= alpha;
                     }
-                    if (!__any_sync(FULL, up)) return true;
+                    if (__builtin_expect(!__any_sync(FULL, up), 1)) return true;
                     // m moved too far for some row: O follows (every P V before this tile is in
                     // it; in a segment's first tile there is nothing yet), and this tile's P
                     uint32_t x[16];
@@ -869,48 +913,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         fewer_regs<kConvRegs>();
         // ====================== converters ======================
         // four warps turn K tiles, four V tiles
-        const int kv = warp >= kConvWarp0 + kConvWarps / 2;
         const int ct = (threadIdx.x - 32 * kConvWarp0) & (kConvThreads - 1);
-        const CacheTensor &t = kv ? p.v : p.k;
-        const float tensor = p.fmt == KVQ_FMT_TENSOR ? __half2float(t.scales[0]) : 1.f;
-        const int bufs = kv ? VB : KB;
-        uint8_t *tiles = smem + (kv ? p.l.off_v : p.l.off_k);
-        const uint32_t tile_bytes = kv ? p.l.v_bytes : p.l.k_bytes;
-        uint64_t *ready = kv ? ctl->vfull : ctl->kfull, *used = kv ? ctl->pvdone[1] : ctl->sfull[1];
-        bool ok = true;
-        int s = kv, use = 0, i = 0;
-        Walk it;
-#pragma unroll 1
-        for (it.start(p, w); it.count && ok; it.next(p)) {
-#pragma unroll 1
-            for (int k = 0; k < it.count; k++, i++) {
-                const int nv = min(TT, it.s.total - (it.tile + k) * TT);
-                ok = wait(&ctl->full[s], use);
-                // the operand's last use: S, or P V, of tile i - bufs
-                if (ok && i >= bufs) ok = wait(&used[(i - bufs) & 1], (i - bufs) >> 1);
-                if (!ok) break;
-                const uint8_t *entry = smem + (uint32_t)s * p.l.entry_bytes;
-                const int buf = i & (bufs - 1);
-                if (kv)
-                    convert_any<DH, true>(p, entry, tiles + (uint32_t)buf * tile_bytes, nv, ct, tensor, par->lv[i & 3],
-                                          par->iv[i & 3]);
-                else
-                    convert_any<DH, false>(p, entry, tiles + (uint32_t)buf * tile_bytes, nv, ct, tensor, par->sk[i & 3],
-                                           nullptr);
-                fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&ctl->par[i & 3]);       // before the tile can be used, so that its
-                    mbar_arrive(&ready[buf]);            // phase is over when the slot comes round
-                    mbar_arrive(&ctl->empty[s]);
-                }
-                s += 2;
-                if (s >= E) {
-                    s -= E;
-                    ++use;
-                }
-            }
-        }
+        const bool ok = warp < kConvWarp0 + kConvWarps / 2
+                            ? convert_role<DH, false>(p, w, smem, ctl, par, ct, abort_flag, limit)
+                            : convert_role<DH, true>(p, w, smem, ctl, par, ct, abort_flag, limit);
         if (!ok) give_up();
     } else {
         fewer_regs<kIssueRegs>();
