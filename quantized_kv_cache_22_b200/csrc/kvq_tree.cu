@@ -60,7 +60,7 @@ __device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.
 template <int N>
 __device__ __forceinline__ void fewer_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-constexpr uint32_t COL_S = 0, COL_O = 128, COL_Q = 384, COL_QLO = 448;   // TMEM columns; S, O: two groups
+constexpr uint32_t COL_S = 0, COL_O = 128, COL_Q = 384, COL_QLO = 448, COL_P = 448;   // TMEM columns; S, O, P: two groups
 constexpr uint32_t PANEL = TT * 128;    // 64 f16 of every token
 
 // P in [0, 2^14]: m starts 6 to 7 below the first chunk's maximum and follows when 14 is passed
@@ -73,7 +73,7 @@ struct Work {
 };
 struct Ctl {
     uint64_t full[kMaxEntries], empty[kMaxEntries];
-    uint64_t kfull[2], vfull[2], sfull[2][2], pfull[2][2], pvdone[2][2], par[4], qfull, soft, drain;
+    uint64_t kfull[2], vfull[2], sfull[2][2], sfree[2][2], pfull[2][2], pvdone[2][2], par[4], qfull, drain;
     Work w;
     uint32_t tmem;
     int abort;
@@ -597,13 +597,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             mbar_init(&ctl->vfull[j], kConvWarps / 2);
             for (int g = 0; g < 2; g++) {
                 mbar_init(&ctl->sfull[g][j], 1);
+                mbar_init(&ctl->sfree[g][j], kSoftWarps);
                 mbar_init(&ctl->pfull[g][j], kSoftWarps);
                 mbar_init(&ctl->pvdone[g][j], 1);
             }
         }
         for (int j = 0; j < 4; j++) mbar_init(&ctl->par[j], kConvWarps);
         mbar_init(&ctl->qfull, kSoftWarps);
-        mbar_init(&ctl->soft, 2 * kSoftWarps);
         mbar_init(&ctl->drain, 1);
         ctl->abort = 0;
         fence_mbar_init();
@@ -621,6 +621,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     const Work w = ctl->w;
     const uint32_t tmem = ctl->tmem;
     const int n_units = w.n_units;
+    // P has columns of its own, unless the second part of fp32 queries takes them: then it lies
+    // over its scores, which then wait for it
+    const bool over = p.q_dtype == KVQ_F32;
 
     if (warp < 2 * kSoftWarps) {
         more_regs<kSoftRegs>();
@@ -633,12 +636,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         const uint32_t s_at = tmem + COL_S + 64u * grp + lane_off, o_at = tmem + COL_O + 128u * grp + lane_off;
         float *stage = reinterpret_cast<float *>(smem + p.l.off_stage);
         const float osign = p.fmt == KVQ_FMT_TENSOR && __half2float(p.v.scales[0]) < 0.f ? -1.f : 1.f;
+        const uint32_t p_row = over ? s_at : tmem + COL_P + 32u * grp + lane_off;
+        // A wait that gave up does not end the role: the eight warps meet at a hardware barrier
+        // at every segment's end, so all of them walk on to the end (with the abort flag up no
+        // further wait takes time) and write nothing more.
         bool ok = true;
-        int syncs = 0;
-        auto soft_sync = [&]() {                     // the eight warps meet
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl->soft);
-            return wait(&ctl->soft, syncs++);
+        auto hold = [&](uint64_t *bar, int parity) {
+            if (!wait(bar, parity) && ok) {
+                ok = false;
+                give_up();
+            }
+        };
+        auto soft_sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(64 * kSoftWarps) : "memory"); };
+        auto blank = [&](uint32_t at, int tb, int chunks) {
+            uint32_t none[8];
+#pragma unroll
+            for (int x = 0; x < 8; x++) none[x] = 0u;
+#pragma unroll 1
+            for (int c = chunks; c < 4; c++) tmem_st8(at + (((uint32_t)tb / 2 + 8u * c) & 31u), none);
         };
         // What a thread keeps of its row; the next segment's is made while the last tile of the
         // current one is with the tensor cores.
@@ -674,67 +689,57 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 return pow2i(-ex);
             };
             if (p.q_dtype == KVQ_F16 && grp == 1) return x;
-            // 16 elements of the row from element d, as fp32
-            auto load16 = [&](int d, float (&e)[16]) {
-                if (!live) {
+            if (p.q_dtype != KVQ_F32) {
+                // the whole row at once, one wait for memory
+                uint4 u[DH / 8];
+                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + at);
 #pragma unroll
-                    for (int k = 0; k < 16; k++) e[k] = 0.f;
-                } else if (p.q_dtype == KVQ_F32) {
-                    const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + at + d);
+                for (int k = 0; k < DH / 8; k++) u[k] = live ? src[k] : make_uint4(0u, 0u, 0u, 0u);
+                uint32_t *h = reinterpret_cast<uint32_t *>(u);
+                if (p.q_dtype == KVQ_BF16) {
+                    // (bf16 magnitudes compare as integers, the high one of a pair above its low one)
+                    uint32_t top = 0u, low = 0u;
 #pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        const float4 f = src[k];
-                        e[4 * k] = f.x; e[4 * k + 1] = f.y; e[4 * k + 2] = f.z; e[4 * k + 3] = f.w;
+                    for (int k = 0; k < DH / 2; k++) {
+                        top = max(top, h[k] & 0x7fff0000u);
+                        low = max(low, h[k] & 0x00007fffu);
                     }
-                } else {
-                    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + at + d);
+                    const float pre = level(__uint_as_float(max(top, low << 16)));
+                    if (grp == 1) return x;
 #pragma unroll
-                    for (int k = 0; k < 2; k++) {
-                        const uint4 u = src[k];
-                        const uint32_t ww[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                        for (int y = 0; y < 4; y++) {
-                            const float2 h = unpack_half2(ww[y]);
-                            const bool half = p.q_dtype == KVQ_F16;
-                            e[8 * k + 2 * y] = half ? h.x : __uint_as_float(ww[y] << 16);
-                            e[8 * k + 2 * y + 1] = half ? h.y : __uint_as_float(ww[y] & 0xffff0000u);
-                        }
-                    }
+                    for (int k = 0; k < DH / 2; k++)
+                        h[k] = pack_half2(__uint_as_float(h[k] << 16) * pre, __uint_as_float(h[k] & 0xffff0000u) * pre);
                 }
-            };
-            if (live) {
-                // the row's lines, all at once: the loops below find them in L1
-                const char *src = static_cast<const char *>(p.q) + at * (p.q_dtype == KVQ_F32 ? 4 : 2);
-                const int bytes = DH * (p.q_dtype == KVQ_F32 ? 4 : 2);
-                for (int k = 0; k < bytes; k += 128) asm volatile("prefetch.global.L1 [%0];" ::"l"(src + k));
-            }
-            float pre = 1.f;
-            if (p.q_dtype != KVQ_F16) {
+#pragma unroll
+                for (int k = 0; k < DH / 32; k++)
+                    tmem_st16(tmem + COL_Q + lane_off + 16u * k, *reinterpret_cast<uint32_t(*)[16]>(h + 16 * k));
+            } else {
+                const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + at);
+                const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
                 float a = 0.f;
-#pragma unroll 1
-                for (int d = 0; d < DH; d += 16) {
-                    float e[16];
-                    load16(d, e);
-#pragma unroll
-                    for (int k = 0; k < 16; k++) a = fmaxf(a, fabsf(e[k]));
+#pragma unroll 8
+                for (int k = 0; k < DH / 4; k++) {
+                    const float4 f = live ? src[k] : none;
+                    a = fmaxf(fmaxf(a, fmaxf(fabsf(f.x), fabsf(f.y))), fmaxf(fabsf(f.z), fabsf(f.w)));
                 }
-                pre = level(a);
+                const float pre = level(a);
                 if (grp == 1) return x;
-            }
 #pragma unroll 1
-            for (int d = 0; d < DH; d += 16) {
-                float e[16];
-                uint32_t hi[8], lo[8];
-                load16(d, e);
+                for (int c = 0; c < DH / 32; c++) {
+                    uint32_t hi[16], lo[16];
 #pragma unroll
-                for (int k = 0; k < 8; k++) {
-                    const float y0 = e[2 * k] * pre, y1 = e[2 * k + 1] * pre;
-                    hi[k] = pack_half2(y0, y1);
-                    const float2 b = unpack_half2(hi[k]);
-                    lo[k] = pack_half2(y0 - b.x, y1 - b.y);
+                    for (int k = 0; k < 8; k++) {
+                        float4 f = live ? src[8 * c + k] : none;
+                        f.x *= pre; f.y *= pre; f.z *= pre; f.w *= pre;
+                        hi[2 * k] = pack_half2(f.x, f.y);
+                        hi[2 * k + 1] = pack_half2(f.z, f.w);
+                        const float2 b0 = unpack_half2(hi[2 * k]), b1 = unpack_half2(hi[2 * k + 1]);
+                        lo[2 * k] = pack_half2(f.x - b0.x, f.y - b0.y);
+                        lo[2 * k + 1] = pack_half2(f.z - b1.x, f.w - b1.y);
+                    }
+                    tmem_st16(tmem + COL_Q + lane_off + 16u * c, hi);
+                    tmem_st16(tmem + COL_QLO + lane_off + 16u * c, lo);
                 }
-                tmem_st8(tmem + COL_Q + lane_off + d / 2, hi);
-                if (p.q_dtype == KVQ_F32) tmem_st8(tmem + COL_QLO + lane_off + d / 2, lo);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -756,16 +761,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             for (int k = 0; k < count; k++, i++) {
                 // ---- P of this thread's tokens, over the columns of their scores
                 const int j = i & 1;
-                ok = wait(&ctl->par[i & 3], i >> 2) && wait(&ctl->sfull[grp][j], i >> 1);
-                if (!ok) break;
+                hold(&ctl->par[i & 3], i >> 2);
+                hold(&ctl->sfull[grp][j], i >> 1);
                 tc_fence_after();
                 const int at = HT * grp + tb;
                 const float *sk = par->sk[i & 3] + at, *lv = par->lv[i & 3] + at, *iv = par->iv[i & 3] + at;
                 const int t0 = (it.tile + k) * TT + HT * grp;
                 const bool whole = t0 + HT <= it.s.len;
-                const uint32_t p_at = s_at + (uint32_t)tb / 2;
-                // raise m to fit a maximum; false: a wait gave up
-                auto fit = [&](float mx, int c) -> bool {
+                const uint32_t p_at = p_row + (uint32_t)tb / 2;
+                // raise m to fit a maximum
+                auto fit = [&](float mx, int c) {
                     const bool set = m == -INFINITY && mx > -INFINITY, up = !set && mx > m + kMoveAt;
                     float alpha = 1.f;
                     if (set || up) {
@@ -774,12 +779,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                         m = to;
                         l *= alpha;
                     }
-                    if (__builtin_expect(!__any_sync(FULL, up), 1)) return true;
+                    if (__builtin_expect(!__any_sync(FULL, up), 1)) return;
                     // m moved too far for some row: O follows (every P V before this tile is in
                     // it; in a segment's first tile there is nothing yet), and this tile's P
                     uint32_t x[16];
                     if (k > 0) {
-                        if (!wait(&ctl->pvdone[grp][j ^ 1], (i - 1) >> 1)) return false;
+                        hold(&ctl->pvdone[grp][j ^ 1], (i - 1) >> 1);
                         tc_fence_after();
 #pragma unroll 1
                         for (int q = 0; q < DH / 16; q++) {
@@ -799,7 +804,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                         for (int q = 0; q < 8; q++) y[q] = hmul2_u32(y[q], alpha2);
                         tmem_st8(p_at + 8u * n, y);
                     }
-                    return true;
                 };
                 // 16 tokens at a time; the next ones' scores are on their way meanwhile
                 const int chunks = 4 / copies;
@@ -812,34 +816,37 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                     tmem_ld16_wait(a);
                     const uint32_t vis = whole ? FULL : visible(t0 + tb + 16 * c, it.s.len, row.mask) | 0xffff0000u;
                     const float mx = scores<16>(a, sk + 16 * c, lv + 16 * c, row.rf, vis, z);
-                    if (c + 1 < chunks) tmem_ld16_async(s_at + tb + 16u * (c + 1), a);
-                    if (!(ok = fit(mx, c))) break;
+                    if (c + 1 < chunks) {
+                        tmem_ld16_async(s_at + tb + 16u * (c + 1), a);
+                    } else if (!over) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ctl->sfree[grp][j]);
+                    }
+                    fit(mx, c);
                     l += probs<16>(z, iv + 16 * c, m == -INFINITY ? 0.f : m, pw);
-                    // (columns of scores that are already read: P takes half as many)
+                    // its columns: of scores that are read (P takes half as many), or of the P before,
+                    // which its product has to be done with
+                    if (c == 0 && k > 0 && !over) {
+                        hold(&ctl->pvdone[grp][j ^ 1], (i - 1) >> 1);
+                        tc_fence_after();
+                    }
                     tmem_st8(p_at + 8u * c, pw);
                 }
-                if (!ok) break;
-                if (copies > 1) {
-                    // the other copies' tokens
-                    uint32_t none[8];
-#pragma unroll
-                    for (int x = 0; x < 8; x++) none[x] = 0u;
-#pragma unroll 1
-                    for (int c = chunks; c < 4; c++) tmem_st8(s_at + (((uint32_t)tb / 2 + 8u * c) & 31u), none);
-                }
+                // zeros for the other copies' tokens: scores left theirs, or they are there already
+                if (copies > 1 && (over || k == 0)) blank(p_row, tb, chunks);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->pfull[grp][j]);
             }
-            if (!ok) break;
             // ---- the next segment's queries come in once both groups' scores are done
             const int last = i - 1;
             Walk ahead = it;
             if (opened) {
                 ahead.next(p);
                 if (ahead.count && grp == 0) {
-                    if (!(ok = wait(&ctl->sfull[1][last & 1], last >> 1))) break;
+                    hold(&ctl->sfull[1][last & 1], last >> 1);
                     tc_fence_after();
                 }
             }
@@ -853,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             // join the groups and copies of every row; the output, or a partial
             const int nr = TT / copies, r = place & (nr - 1), rows = row.rows;
             ctl->ml[grp][place] = make_float2(m, l);
-            if (!(ok = soft_sync())) break;
+            soft_sync();
             float M = -INFINITY, L = 0.f;
 #pragma unroll 1
             for (int c = r; c < 2 * TT; c += nr) M = fmaxf(M, ctl->ml[0][c].x);
@@ -869,12 +876,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             float *part = p.slots + (int64_t)slot * tree_slot_floats(p.slot_rows, DH);
             float f = m == -INFINITY ? 0.f : ex2(m - M) * osign;
             if (direct) f = L != 0.f ? f / L : 0.f;
-            if (threadIdx.x == 0 && opens)
+            if (threadIdx.x == 0 && opens && ok)
                 p.seg[((int64_t)it.b * p.rows.heads + it.head) * p.row_tiles + it.rt] =
                     make_int4(slot, blockIdx.x, direct ? 1 : range_cta(u1 - 1, w.n, w.p) - (int)blockIdx.x + 1, 0);
             if (!direct && threadIdx.x < rows)
                 *reinterpret_cast<float2 *>(part + (int64_t)p.slot_rows * DH + 2 * place) = make_float2(M, L);
-            if (!(ok = wait(&ctl->pvdone[grp][last & 1], last >> 1))) break;
+            hold(&ctl->pvdone[grp][last & 1], last >> 1);
             tc_fence_after();
             // four columns of a row a thread: rows threadIdx.x / 4 and, of more than 64, + 64
             const int r0 = threadIdx.x >> 2, col = (threadIdx.x & 3) * 4;
@@ -883,13 +890,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             for (int c = 0; c < DH / 16; c++) {
                 uint32_t o[16];
                 tmem_ld16(o_at + 16u * c, o);
-                if (c > 0 && !(ok = soft_sync())) break;             // the staging was read
+                if (c > 0) soft_sync();                              // the staging was read
 #pragma unroll
                 for (int x = 0; x < 16; x++)
                     stage[(grp * TT + place) * STAGE_LD + x] = f == 0.f ? 0.f : __uint_as_float(o[x]) * f;
-                if (!(ok = soft_sync())) break;
+                soft_sync();
 #pragma unroll 1
-                for (int k = 0; k < 2; k++) {
+                for (int k = 0; k < 2 && ok; k++) {
                     const int rr = r0 + 64 * k;
                     if (rr >= rows) break;
                     float y[4] = {0.f, 0.f, 0.f, 0.f};
@@ -904,11 +911,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                         *reinterpret_cast<float4 *>(part + rr * DH + col + 16 * c) = make_float4(y[0], y[1], y[2], y[3]);
                 }
             }
-            if (!ok) break;
             row = next;
             it = ahead;
         }
-        if (!ok) give_up();
     } else if (warp >= kConvWarp0) {
         fewer_regs<kConvRegs>();
         // ====================== converters ======================
@@ -1004,7 +1009,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 #pragma unroll 1
                 for (int part = 0; part <= p.l.v_grouped; part++) {
                     const uint64_t d = v_desc + (vb * (p.l.v_bytes >> 4) + part * lo + g * (HT * 128u >> 4));
-                    const uint32_t ot = tm + COL_O + 128u * g, pa = tm + COL_S + 64u * g;
+                    const uint32_t ot = tm + COL_O + 128u * g, pa = tm + (over ? COL_S + 64u * g : COL_P + 32u * g);
                     if (leader)
 #pragma unroll
                         for (int kk = 0; kk < HT / 16; kk++)
@@ -1023,12 +1028,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 const int count = __shfl_sync(FULL, it.count, 0);
                 // a new segment's queries replace the old ones: its scores wait for them
                 ok = wait(&ctl->qfull, seg++) && issue_s(i, 0) && issue_s(i, 1);
-                // a group's scores of the next tile follow its P V of this one (they share columns)
 #pragma unroll 1
                 for (int k = 0; k < count && ok; k++, i++) {
                     const bool more = k + 1 < count;
+                    // the next tile's scores as soon as a group has read this one's
 #pragma unroll 1
-                    for (int g = 0; g < 2 && ok; g++) ok = issue_pv(i, g, k == 0) && (!more || issue_s(i + 1, g));
+                    for (int g = 0; g < 2 && ok && more && !over; g++)
+                        ok = wait(&ctl->sfree[g][i & 1], i >> 1) && issue_s(i + 1, g);
+#pragma unroll 1
+                    for (int g = 0; g < 2 && ok; g++)
+                        ok = issue_pv(i, g, k == 0) && (!more || !over || issue_s(i + 1, g));
                 }
             }
             if (!ok) give_up();
