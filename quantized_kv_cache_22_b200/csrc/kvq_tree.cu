@@ -99,11 +99,28 @@ __device__ __forceinline__ float lg2(float x)
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// A launch parameter that a role uses in every tile, held in a register: left alone, the
+// compiler reads it from the constant bank at each use, and a warp that runs alone waits there.
+template <class X>
+__device__ __forceinline__ X keep(X x)
+{
+    static_assert(sizeof(X) == 4, "one register");
+    asm volatile("" : "+r"(x));
+    return x;
+}
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
+// Wait for the phase of the given parity, giving up after limit ns or when the abort flag is
+// up.  (No suspend-time hint: with one the wait becomes a polling loop of its own, whose
+// instructions cost the other warps of the SM more than the wait does.)
 __device__ __forceinline__ bool wait_bounded(uint64_t *bar, int parity, int *abort_flag, uint64_t limit)
 {
-    return mbar_wait_bounded(bar, parity & 1, abort_flag, limit);
+    if (mbar_try_wait(bar, parity & 1)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    do {
+        if (mbar_try_wait(bar, parity & 1)) return true;
+    } while (!*static_cast<volatile int *>(abort_flag) && globaltimer_ns() - t0 < limit);
+    return false;
 }
 // a wait of a whole warp: its lanes go on, or give up, together
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, int parity, int *abort_flag, uint64_t limit)
@@ -427,12 +444,13 @@ __device__ __forceinline__ bool convert_tiles(const TreeParams &p, const Work &w
                                               int ct, int *abort_flag, uint64_t limit)
 {
     const CacheTensor &ten = ISV ? p.v : p.k;
-    const int ng = DH / ten.group, gshift = ten.group == 32 ? 5 : ten.group == 64 ? 6 : 7;
-    const bool is_tensor = p.fmt == KVQ_FMT_TENSOR;
+    const int ng = keep(DH / ten.group), gshift = ten.group == 32 ? 5 : ten.group == 64 ? 6 : 7;
+    const bool is_tensor = keep(p.fmt) == KVQ_FMT_TENSOR;
     const float tensor = is_tensor ? __half2float(ten.scales[0]) : 1.f;
-    const int bufs = ISV ? p.l.v_bufs : p.l.k_bufs, E = p.l.entries;
-    uint8_t *tiles = smem + (ISV ? p.l.off_v : p.l.off_k);
-    const uint32_t tile_bytes = ISV ? p.l.v_bytes : p.l.k_bytes;
+    const int bufs = keep(ISV ? p.l.v_bufs : p.l.k_bufs), E = keep(p.l.entries);
+    uint8_t *tiles = smem + keep(ISV ? p.l.off_v : p.l.off_k);
+    const uint32_t tile_bytes = keep(ISV ? p.l.v_bytes : p.l.k_bytes), entry_bytes = keep(p.l.entry_bytes);
+    const uint32_t off_scales = keep(p.l.off_scales), lo = keep(p.l.lo);
     uint64_t *ready = ISV ? ctl->vfull : ctl->kfull, *used = ISV ? ctl->pvdone[1] : ctl->sfull[1];
     int s = ISV, use = 0, i = 0;
     Walk it;
@@ -444,10 +462,10 @@ __device__ __forceinline__ bool convert_tiles(const TreeParams &p, const Work &w
             if (!wait_warp(&ctl->full[s], use, abort_flag, limit)) return false;
             // the operand's last use: S, or P V, of tile i - bufs
             if (i >= bufs && !wait_warp(&used[(i - bufs) & 1], (i - bufs) >> 1, abort_flag, limit)) return false;
-            const uint8_t *entry = smem + (uint32_t)s * p.l.entry_bytes;
+            const uint8_t *entry = smem + (uint32_t)s * entry_bytes;
             const int buf = i & (bufs - 1);
-            convert<DH, KIND, GRP, ISV>(entry, reinterpret_cast<const uint16_t *>(entry + p.l.off_scales),
-                                        tiles + (uint32_t)buf * tile_bytes, p.l.lo, min(TT, left), ct, ng, gshift, tensor,
+            convert<DH, KIND, GRP, ISV>(entry, reinterpret_cast<const uint16_t *>(entry + off_scales),
+                                        tiles + (uint32_t)buf * tile_bytes, lo, min(TT, left), ct, ng, gshift, tensor,
                                         is_tensor, ISV ? par->lv[i & 3] : par->sk[i & 3], par->iv[i & 3]);
             fence_proxy_async_shared();
             __syncwarp();
@@ -574,11 +592,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     constexpr uint32_t IDESC_O = (1u << 4) | (1u << 16) | ((uint32_t)(DH >> 3) << 17) | ((128u >> 4) << 24);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-    Ctl *ctl = reinterpret_cast<Ctl *>(smem + p.l.off_ctl);
-    Par *par = reinterpret_cast<Par *>(smem + p.l.off_par);
+    Ctl *ctl = reinterpret_cast<Ctl *>(smem + keep(p.l.off_ctl));
+    Par *par = reinterpret_cast<Par *>(smem + keep(p.l.off_par));
     int *abort_flag = &ctl->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int E = p.l.entries, KB = p.l.k_bufs, VB = p.l.v_bufs;
+    const int E = keep(p.l.entries), KB = keep(p.l.k_bufs), VB = keep(p.l.v_bufs);
     const uint64_t limit = p.timeout_ns;
     auto give_up = [&]() {
         *static_cast<volatile int *>(abort_flag) = 1;
@@ -623,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     const int n_units = w.n_units;
     // P has columns of its own, unless the second part of fp32 queries takes them: then it lies
     // over its scores, which then wait for it
-    const bool over = p.q_dtype == KVQ_F32;
+    const bool over = keep(p.q_dtype) == KVQ_F32;
 
     if (warp < 2 * kSoftWarps) {
         more_regs<kSoftRegs>();
@@ -634,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         const int place = threadIdx.x & (TT - 1);    // TMEM lane
         const uint32_t lane_off = (uint32_t)(place & ~31) << 16;
         const uint32_t s_at = tmem + COL_S + 64u * grp + lane_off, o_at = tmem + COL_O + 128u * grp + lane_off;
-        float *stage = reinterpret_cast<float *>(smem + p.l.off_stage);
+        float *stage = reinterpret_cast<float *>(smem + keep(p.l.off_stage));
         const float osign = p.fmt == KVQ_FMT_TENSOR && __half2float(p.v.scales[0]) < 0.f ? -1.f : 1.f;
         const uint32_t p_row = over ? s_at : tmem + COL_P + 32u * grp + lane_off;
         // A wait that gave up does not end the role: the eight warps meet at a hardware barrier
@@ -978,18 +996,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             const bool leader = elect_one();
             const uint32_t tm = __shfl_sync(FULL, tmem, 0);
             const uint32_t sbase = smem_u32(smem);
-            const uint64_t k_desc = sw128_desc(sbase + p.l.off_k), v_desc = sw128_mn_desc(sbase + p.l.off_v, PANEL, 1024u);
-            const uint32_t lo = p.l.lo >> 4;          // descriptors count 16-byte units
-            const int q_parts = p.q_dtype == KVQ_F32 ? 2 : 1;
+            const uint64_t k_desc = sw128_desc(sbase + keep(p.l.off_k)), v_desc = sw128_mn_desc(sbase + keep(p.l.off_v), PANEL, 1024u);
+            // (descriptors count 16-byte units)
+            const uint32_t lo = keep(p.l.lo) >> 4, k_step = keep(p.l.k_bytes) >> 4, v_step = keep(p.l.v_bytes) >> 4;
+            const int q_parts = over ? 2 : 1, s_parts = (1 + keep(p.l.k_grouped)) * q_parts, v_parts = 1 + keep(p.l.v_grouped);
             // scores of tile i for group g's half of its tokens
             auto issue_s = [&](int i, int g) {
                 const int kb = i & (KB - 1);
                 if (!wait(&ctl->kfull[kb], i >> (KB - 1))) return false;
                 tc_fence_after();
 #pragma unroll 1
-                for (int part = 0; part < (1 + p.l.k_grouped) * q_parts; part++) {
+                for (int part = 0; part < s_parts; part++) {
                     const int kp = q_parts == 2 ? part >> 1 : part, qp = q_parts == 2 ? part & 1 : 0;
-                    const uint64_t d = k_desc + (kb * (p.l.k_bytes >> 4) + kp * lo + g * (HT * 128u >> 4));
+                    const uint64_t d = k_desc + (kb * k_step + kp * lo + g * (HT * 128u >> 4));
                     const uint32_t qa = tm + (qp ? COL_QLO : COL_Q), st = tm + COL_S + 64u * g;
                     if (leader)
 #pragma unroll
@@ -1007,8 +1026,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 if (!wait(&ctl->vfull[vb], i >> (VB - 1)) || !wait(&ctl->pfull[g][i & 1], i >> 1)) return false;
                 tc_fence_after();
 #pragma unroll 1
-                for (int part = 0; part <= p.l.v_grouped; part++) {
-                    const uint64_t d = v_desc + (vb * (p.l.v_bytes >> 4) + part * lo + g * (HT * 128u >> 4));
+                for (int part = 0; part < v_parts; part++) {
+                    const uint64_t d = v_desc + (vb * v_step + part * lo + g * (HT * 128u >> 4));
                     const uint32_t ot = tm + COL_O + 128u * g, pa = tm + (over ? COL_S + 64u * g : COL_P + 32u * g);
                     if (leader)
 #pragma unroll
