@@ -53,7 +53,7 @@ constexpr unsigned FULL = 0xffffffffu;
 
 // Registers a thread: the block starts with 96 x 640 threads and shares them out anew by
 // warpgroup (2 x softmax, producer and issuer, 2 x converters: 480 in all, as launched).
-constexpr int kSoftRegs = 128, kIssueRegs = 64, kConvRegs = 80;
+constexpr int kSoftRegs = 128, kIssueRegs = 48, kConvRegs = 88;
 static_assert(2 * kSoftRegs + kIssueRegs + 2 * kConvRegs == 5 * 96, "the shares add up to the launch");
 template <int N>
 __device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -73,7 +73,10 @@ struct Work {
 };
 struct Ctl {
     uint64_t full[kMaxEntries], empty[kMaxEntries];
-    uint64_t kfull[2], vfull[2], sfull[2][2], sfree[2][2], pfull[2][2], pvdone[2][2], par[4], qfull, drain;
+    // by tile parity: a tile's K is converted and its S columns and queries are in order; its S
+    // is done; its V is converted and its P written; its P V is done
+    uint64_t sready[2], sfull[2], pready[2], pvdone[2];
+    uint64_t par[4], drain;             // a tile's per-token numbers are there (by tile, four deep)
     Work w;
     uint32_t tmem;
     int abort;
@@ -83,6 +86,10 @@ struct Ctl {
 // the softmax.
 struct Par {
     float sk[4][TT], lv[4][TT], iv[4][TT];
+};
+template <int N>
+struct Int {
+    static constexpr int value = N;
 };
 constexpr int STAGE_LD = 17;            // floats per row of the epilogue's 16-column staging
 constexpr int STAGE_BYTES = 2 * TT * STAGE_LD * 4;
@@ -360,7 +367,7 @@ __device__ __forceinline__ void convert(const uint8_t *raw, const uint16_t *sc, 
                 // P = 0 where the token is masked, so it has to be a number)
                 if (s == 0.f || bad || t >= nvalid) s = 1.f;
                 p0[t] = bad ? __int_as_float(0x7fc00000) : lg2(s);
-                p1[t] = __frcp_rn(s);
+                p1[t] = __fdividef(1.f, s);
             } else {
                 p0[t] = s;
             }
@@ -371,8 +378,7 @@ __device__ __forceinline__ void convert(const uint8_t *raw, const uint16_t *sc, 
     const uint8_t *src = raw + tr * ROW + c * Raw<KIND>::BYTES;
     uint8_t *out = dst + tr * 128 + ((c ^ tr) & 7) * 16;      // (t ^ tr) & 7 = 0: RPP is a multiple of 8
     uint32_t bad_rows = 0;                                     // CHECK: bit u for pass u
-    // (kept a loop: the roles' code together has to stay within the instruction cache)
-#pragma unroll 1
+#pragma unroll
     for (int pn = 0; pn < PANELS; pn++) {
         const int panel = PANELS == 2 ? pn ^ turn : 0;
         const int g = (c * 8 + 64 * panel) >> gshift;
@@ -451,7 +457,7 @@ __device__ __forceinline__ bool convert_tiles(const TreeParams &p, const Work &w
     uint8_t *tiles = smem + keep(ISV ? p.l.off_v : p.l.off_k);
     const uint32_t tile_bytes = keep(ISV ? p.l.v_bytes : p.l.k_bytes), entry_bytes = keep(p.l.entry_bytes);
     const uint32_t off_scales = keep(p.l.off_scales), lo = keep(p.l.lo);
-    uint64_t *ready = ISV ? ctl->vfull : ctl->kfull, *used = ISV ? ctl->pvdone[1] : ctl->sfull[1];
+    uint64_t *ready = ISV ? ctl->pready : ctl->sready, *used = ISV ? ctl->pvdone : ctl->sfull;
     int s = ISV, use = 0, i = 0;
     Walk it;
 #pragma unroll 1
@@ -471,7 +477,7 @@ __device__ __forceinline__ bool convert_tiles(const TreeParams &p, const Work &w
             __syncwarp();
             if ((ct & 31) == 0) {
                 mbar_arrive(&ctl->par[i & 3]);       // before the tile can be used, so that its
-                mbar_arrive(&ready[buf]);            // phase is over when the slot comes round
+                mbar_arrive(&ready[i & 1]);          // phase is over when the slot comes round
                 mbar_arrive(&ctl->empty[s]);
             }
             s += 2;
@@ -588,7 +594,7 @@ __device__ __forceinline__ float probs(const uint64_t (&z)[N / 2], const float *
 template <int DH>
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p)
 {
-    constexpr uint32_t IDESC_S = (1u << 4) | ((uint32_t)(HT >> 3) << 17) | ((128u >> 4) << 24);
+    constexpr uint32_t IDESC_S = (1u << 4) | ((uint32_t)(TT >> 3) << 17) | ((128u >> 4) << 24);
     constexpr uint32_t IDESC_O = (1u << 4) | (1u << 16) | ((uint32_t)(DH >> 3) << 17) | ((128u >> 4) << 24);
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -611,17 +617,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             mbar_init(&ctl->empty[s], kConvWarps / 2);
         }
         for (int j = 0; j < 2; j++) {
-            mbar_init(&ctl->kfull[j], kConvWarps / 2);
-            mbar_init(&ctl->vfull[j], kConvWarps / 2);
-            for (int g = 0; g < 2; g++) {
-                mbar_init(&ctl->sfull[g][j], 1);
-                mbar_init(&ctl->sfree[g][j], kSoftWarps);
-                mbar_init(&ctl->pfull[g][j], kSoftWarps);
-                mbar_init(&ctl->pvdone[g][j], 1);
-            }
+            mbar_init(&ctl->sready[j], kConvWarps / 2 + 2 * kSoftWarps);
+            mbar_init(&ctl->sfull[j], 1);
+            mbar_init(&ctl->pready[j], kConvWarps / 2 + 2 * kSoftWarps);
+            mbar_init(&ctl->pvdone[j], 1);
         }
         for (int j = 0; j < 4; j++) mbar_init(&ctl->par[j], kConvWarps);
-        mbar_init(&ctl->qfull, kSoftWarps);
         mbar_init(&ctl->drain, 1);
         ctl->abort = 0;
         fence_mbar_init();
@@ -647,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         more_regs<kSoftRegs>();
         // ====================== softmax ======================
         // two groups of four warps: group g takes tokens 64 g .. 64 g + 63 of every tile, with
-        // an O of its own; while one works on its P the tensor cores work for the other
+        // an O of its own
         const int grp = warp / kSoftWarps;
         const int place = threadIdx.x & (TT - 1);    // TMEM lane
         const uint32_t lane_off = (uint32_t)(place & ~31) << 16;
@@ -760,9 +761,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 }
             }
             tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl->qfull);
             return x;
         };
         Walk it;
@@ -779,8 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             for (int k = 0; k < count; k++, i++) {
                 // ---- P of this thread's tokens, over the columns of their scores
                 const int j = i & 1;
-                hold(&ctl->par[i & 3], i >> 2);
-                hold(&ctl->sfull[grp][j], i >> 1);
+                hold(&ctl->sfull[j], i >> 1);
                 tc_fence_after();
                 const int at = HT * grp + tb;
                 const float *sk = par->sk[i & 3] + at, *lv = par->lv[i & 3] + at, *iv = par->iv[i & 3] + at;
@@ -802,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                     // it; in a segment's first tile there is nothing yet), and this tile's P
                     uint32_t x[16];
                     if (k > 0) {
-                        hold(&ctl->pvdone[grp][j ^ 1], (i - 1) >> 1);
+                        hold(&ctl->pvdone[j ^ 1], (i - 1) >> 1);
                         tc_fence_after();
 #pragma unroll 1
                         for (int q = 0; q < DH / 16; q++) {
@@ -823,53 +820,59 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                         tmem_st8(p_at + 8u * n, y);
                     }
                 };
-                // 16 tokens at a time; the next ones' scores are on their way meanwhile
-                const int chunks = 4 / copies;
-                uint32_t a[16];
-                tmem_ld16_async(s_at + tb, a);
-#pragma unroll 1
-                for (int c = 0; c < chunks; c++) {
-                    uint32_t pw[8];
-                    uint64_t z[8];
-                    tmem_ld16_wait(a);
-                    const uint32_t vis = whole ? FULL : visible(t0 + tb + 16 * c, it.s.len, row.mask) | 0xffff0000u;
-                    const float mx = scores<16>(a, sk + 16 * c, lv + 16 * c, row.rf, vis, z);
-                    if (c + 1 < chunks) {
-                        tmem_ld16_async(s_at + tb + 16u * (c + 1), a);
-                    } else if (!over) {
+                // N tokens from chunk c on: P over the columns of scores that are read (it takes half
+                // as many), or of the P before, which its product has to be done with
+                auto chunk = [&](auto n, int c, bool done) {
+                    constexpr int N = decltype(n)::value;
+                    uint32_t a[N], pw[N / 2];
+                    uint64_t z[N / 2];
+                    tmem_ld_async(s_at + tb + N * c, a);
+                    if (c == 0) hold(&ctl->par[i & 3], i >> 2);
+                    tmem_ld_wait(a);
+                    const int tok = t0 + tb + N * c;
+                    uint32_t vis = FULL;
+                    if (!whole) vis = visible(tok, it.s.len, row.mask) | (N == 32 ? 0u : 0xffff0000u);
+                    const float mx = scores<N>(a, sk + N * c, lv + N * c, row.rf, vis, z);
+                    if (done && !over && k + 1 < count) {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&ctl->sfree[grp][j]);
+                        if (lane == 0) mbar_arrive(&ctl->sready[j ^ 1]);
                     }
-                    fit(mx, c);
-                    l += probs<16>(z, iv + 16 * c, m == -INFINITY ? 0.f : m, pw);
-                    // its columns: of scores that are read (P takes half as many), or of the P before,
-                    // which its product has to be done with
+                    fit(mx, N / 16 * c);
+                    l += probs<N>(z, iv + N * c, m == -INFINITY ? 0.f : m, pw);
                     if (c == 0 && k > 0 && !over) {
-                        hold(&ctl->pvdone[grp][j ^ 1], (i - 1) >> 1);
+                        hold(&ctl->pvdone[j ^ 1], (i - 1) >> 1);
                         tc_fence_after();
                     }
-                    tmem_st8(p_at + 8u * c, pw);
+                    tmem_st_cols(p_at + N / 2 * c, pw);
+                };
+                if (copies == 4) {
+                    chunk(Int<16>(), 0, true);
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < 2 / copies; c++) chunk(Int<32>(), c, c == 2 / copies - 1);
                 }
                 // zeros for the other copies' tokens: scores left theirs, or they are there already
-                if (copies > 1 && (over || k == 0)) blank(p_row, tb, chunks);
+                if (copies > 1 && (over || k == 0)) blank(p_row, tb, 4 / copies);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->pfull[grp][j]);
-            }
-            // ---- the next segment's queries come in once both groups' scores are done
-            const int last = i - 1;
-            Walk ahead = it;
-            if (opened) {
-                ahead.next(p);
-                if (ahead.count && grp == 0) {
-                    hold(&ctl->sfull[1][last & 1], last >> 1);
-                    tc_fence_after();
+                if (lane == 0) {
+                    mbar_arrive(&ctl->pready[j]);
+                    if (over && k + 1 < count) mbar_arrive(&ctl->sready[j ^ 1]);
                 }
             }
+            // ---- the next segment's queries come in: this one's scores are all done
+            const int last = i - 1;
+            Walk ahead = it;
+            if (opened) ahead.next(p);
             Row next{};
-            if (ahead.count) next = open(ahead);
+            if (ahead.count) {
+                next = open(ahead);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->sready[i & 1]);
+            }
             if (!opened) {
                 opened = true;
                 row = next;
@@ -899,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                     make_int4(slot, blockIdx.x, direct ? 1 : range_cta(u1 - 1, w.n, w.p) - (int)blockIdx.x + 1, 0);
             if (!direct && threadIdx.x < rows)
                 *reinterpret_cast<float2 *>(part + (int64_t)p.slot_rows * DH + 2 * place) = make_float2(M, L);
-            hold(&ctl->pvdone[grp][last & 1], last >> 1);
+            hold(&ctl->pvdone[last & 1], last >> 1);
             tc_fence_after();
             // four columns of a row a thread: rows threadIdx.x / 4 and, of more than 64, + 64
             const int r0 = threadIdx.x >> 2, col = (threadIdx.x & 3) * 4;
@@ -999,64 +1002,58 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             const uint64_t k_desc = sw128_desc(sbase + keep(p.l.off_k)), v_desc = sw128_mn_desc(sbase + keep(p.l.off_v), PANEL, 1024u);
             // (descriptors count 16-byte units)
             const uint32_t lo = keep(p.l.lo) >> 4, k_step = keep(p.l.k_bytes) >> 4, v_step = keep(p.l.v_bytes) >> 4;
+            const uint32_t p_col = over ? COL_S : COL_P, p_gap = over ? 32u : 0u;   // P, and what lies between the halves
             const int q_parts = over ? 2 : 1, s_parts = (1 + keep(p.l.k_grouped)) * q_parts, v_parts = 1 + keep(p.l.v_grouped);
-            // scores of tile i for group g's half of its tokens
-            auto issue_s = [&](int i, int g) {
-                const int kb = i & (KB - 1);
-                if (!wait(&ctl->kfull[kb], i >> (KB - 1))) return false;
+            // scores of tile i
+            auto issue_s = [&](int i) {
+                if (!wait(&ctl->sready[i & 1], i >> 1)) return false;
                 tc_fence_after();
 #pragma unroll 1
                 for (int part = 0; part < s_parts; part++) {
                     const int kp = q_parts == 2 ? part >> 1 : part, qp = q_parts == 2 ? part & 1 : 0;
-                    const uint64_t d = k_desc + (kb * k_step + kp * lo + g * (HT * 128u >> 4));
-                    const uint32_t qa = tm + (qp ? COL_QLO : COL_Q), st = tm + COL_S + 64u * g;
+                    const uint64_t d = k_desc + ((i & (KB - 1)) * k_step + kp * lo);
+                    const uint32_t qa = tm + (qp ? COL_QLO : COL_Q);
                     if (leader)
 #pragma unroll
                         for (int kk = 0; kk < DH / 16; kk++)
-                            umma_f16_ts(st, qa + 8u * kk, d + ((kk >> 2) * (PANEL >> 4) + 2u * (kk & 3)), IDESC_S,
+                            umma_f16_ts(tm + COL_S, qa + 8u * kk, d + ((kk >> 2) * (PANEL >> 4) + 2u * (kk & 3)), IDESC_S,
                                         kk > 0 ? 1u : (uint32_t)(part > 0));
                 }
-                if (leader) umma_commit(&ctl->sfull[g][i & 1]);
+                if (leader) umma_commit(&ctl->sfull[i & 1]);
                 __syncwarp();
                 return true;
             };
-            // O += P V of tile i
-            auto issue_pv = [&](int i, int g, bool first) {
-                const int vb = i & (VB - 1);
-                if (!wait(&ctl->vfull[vb], i >> (VB - 1)) || !wait(&ctl->pfull[g][i & 1], i >> 1)) return false;
+            // O += P V of tile i: each softmax group's half of the tokens into its own O
+            auto issue_pv = [&](int i, bool first) {
+                if (!wait(&ctl->pready[i & 1], i >> 1)) return false;
                 tc_fence_after();
 #pragma unroll 1
                 for (int part = 0; part < v_parts; part++) {
-                    const uint64_t d = v_desc + (vb * v_step + part * lo + g * (HT * 128u >> 4));
-                    const uint32_t ot = tm + COL_O + 128u * g, pa = tm + (over ? COL_S + 64u * g : COL_P + 32u * g);
+                    const uint64_t d = v_desc + ((i & (VB - 1)) * v_step + part * lo);
                     if (leader)
 #pragma unroll
-                        for (int kk = 0; kk < HT / 16; kk++)
-                            umma_f16_ts(ot, pa + 8u * kk, d + 128u * kk, IDESC_O,
-                                        kk > 0 ? 1u : (uint32_t)(!first || part > 0));
+                        for (int kk = 0; kk < TT / 16; kk++)
+                            umma_f16_ts(tm + COL_O + (kk < 4 ? 0u : 128u), tm + p_col + 8u * kk + (kk < 4 ? 0u : p_gap),
+                                        d + 128u * kk, IDESC_O, (kk & 3) > 0 ? 1u : (uint32_t)(!first || part > 0));
                 }
-                if (leader) umma_commit(&ctl->pvdone[g][i & 1]);
+                if (leader) umma_commit(&ctl->pvdone[i & 1]);
                 __syncwarp();
                 return true;
             };
-            int i = 0, seg = 0;
+            int i = 0;
             bool ok = true;
             Walk it;
 #pragma unroll 1
             for (it.start(p, w); it.count && ok; it.next(p)) {
                 const int count = __shfl_sync(FULL, it.count, 0);
-                // a new segment's queries replace the old ones: its scores wait for them
-                ok = wait(&ctl->qfull, seg++) && issue_s(i, 0) && issue_s(i, 1);
+                ok = issue_s(i);
 #pragma unroll 1
                 for (int k = 0; k < count && ok; k++, i++) {
+                    // the next tile's scores go first, unless this one's P lies over them
                     const bool more = k + 1 < count;
-                    // the next tile's scores as soon as a group has read this one's
-#pragma unroll 1
-                    for (int g = 0; g < 2 && ok && more && !over; g++)
-                        ok = wait(&ctl->sfree[g][i & 1], i >> 1) && issue_s(i + 1, g);
-#pragma unroll 1
-                    for (int g = 0; g < 2 && ok; g++)
-                        ok = issue_pv(i, g, k == 0) && (!more || !over || issue_s(i + 1, g));
+                    if (more && !over) ok = issue_s(i + 1);
+                    ok = ok && issue_pv(i, k == 0);
+                    if (more && over) ok = ok && issue_s(i + 1);
                 }
             }
             if (!ok) give_up();
