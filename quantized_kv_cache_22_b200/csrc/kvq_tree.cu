@@ -43,8 +43,7 @@ namespace kvq {
 namespace {
 
 constexpr int TT = 128;                 // tokens of a tile
-constexpr int HT = TT / 2;               // tokens of a tile that one softmax group takes
-constexpr int kSoftWarps = 4, kConvWarps = 8;   // a softmax group's warps; converter warps
+constexpr int kSoftWarps = 4, kConvWarps = 8;   // a softmax group's warps (two groups); converter warps
 constexpr int kProducerWarp = 8, kMmaWarp = 9, kConvWarp0 = 12;   // (10 and 11 fill up their warpgroup)
 constexpr int kThreads = 32 * (kConvWarp0 + kConvWarps);
 constexpr int kConvThreads = 16 * kConvWarps;   // of K, and of V
@@ -53,17 +52,18 @@ constexpr unsigned FULL = 0xffffffffu;
 
 // Registers a thread: the block starts with 96 x 640 threads and shares them out anew by
 // warpgroup (2 x softmax, producer and issuer, 2 x converters: 480 in all, as launched).
-constexpr int kSoftRegs = 128, kIssueRegs = 48, kConvRegs = 88;
+constexpr int kSoftRegs = 144, kIssueRegs = 48, kConvRegs = 72;
 static_assert(2 * kSoftRegs + kIssueRegs + 2 * kConvRegs == 5 * 96, "the shares add up to the launch");
 template <int N>
 __device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 __device__ __forceinline__ void fewer_regs() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-constexpr uint32_t COL_S = 0, COL_O = 128, COL_Q = 384, COL_QLO = 448, COL_P = 448;   // TMEM columns; S, O, P: two groups
+// TMEM columns: S of even and of odd tiles, O, Q (and the second part of fp32 queries), P
+constexpr uint32_t COL_S = 0, COL_O = 256, COL_Q = 384, COL_QLO = 448, COL_P = 448;
 constexpr uint32_t PANEL = TT * 128;    // 64 f16 of every token
 
-// P in [0, 2^14]: m starts 6 to 7 below the first chunk's maximum and follows when 14 is passed
+// P in [0, 2^14]: m starts 6 to 7 below the first tile's maximum and follows when 14 is passed
 constexpr float kHead = 6.f, kMoveAt = 14.f;
 
 struct Work {
@@ -73,14 +73,15 @@ struct Work {
 };
 struct Ctl {
     uint64_t full[kMaxEntries], empty[kMaxEntries];
-    // by tile parity: a tile's K is converted and its S columns and queries are in order; its S
-    // is done; its V is converted and its P written; its P V is done
+    // by tile parity: a tile may have its scores (K converted, the S of two tiles before read,
+    // queries in place); S done; V converted and P written; P V done
     uint64_t sready[2], sfull[2], pready[2], pvdone[2];
-    uint64_t par[4], drain;             // a tile's per-token numbers are there (by tile, four deep)
+    uint64_t par[4], drain;             // V's per-token numbers of a tile are there (four deep)
     Work w;
     uint32_t tmem;
     int abort;
-    float2 ml[2][TT];
+    float m[TT];                        // what O is scaled by, per TMEM lane
+    float2 ml[2][TT];                   // (m, l) of the groups
 };
 // Per-token numbers of a tile, four tiles deep: the converters run at most two tiles ahead of
 // the softmax.
@@ -118,21 +119,31 @@ __device__ __forceinline__ X keep(X x)
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
 // Wait for the phase of the given parity, giving up after limit ns or when the abort flag is
-// up.  (No suspend-time hint: with one the wait becomes a polling loop of its own, whose
-// instructions cost the other warps of the SM more than the wait does.)
+// up.  A try returns at once when barriers change, which they do all the time in this kernel,
+// and a waiting warp's tries take issue slots from the others: so it sleeps a little between
+// them (NAP nanoseconds), longer where the role runs ahead of need anyway.
+constexpr int kShortNap = 20, kLongNap = 100;
+template <int NAP>
 __device__ __forceinline__ bool wait_bounded(uint64_t *bar, int parity, int *abort_flag, uint64_t limit)
 {
-    if (mbar_try_wait(bar, parity & 1)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    do {
-        if (mbar_try_wait(bar, parity & 1)) return true;
-    } while (!*static_cast<volatile int *>(abort_flag) && globaltimer_ns() - t0 < limit);
-    return false;
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (;;) {
+#pragma unroll 1
+        for (int n = 0; n < 64; n++) {
+            if (mbar_try_wait(bar, parity & 1)) return true;
+            __nanosleep(NAP);
+        }
+        const uint64_t t = globaltimer_ns();
+        if (t0 == 0) t0 = t;
+        if (*static_cast<volatile int *>(abort_flag) || t - t0 > limit) return false;
+    }
 }
 // a wait of a whole warp: its lanes go on, or give up, together
+template <int NAP>
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, int parity, int *abort_flag, uint64_t limit)
 {
-    return __all_sync(FULL, wait_bounded(bar, parity, abort_flag, limit)) != 0;
+    return __all_sync(FULL, wait_bounded<NAP>(bar, parity, abort_flag, limit)) != 0;
 }
 
 // ------------------------------------------------------------------ work split
@@ -327,8 +338,40 @@ __device__ __forceinline__ RowScale row_scale(const uint16_t *sc, int t, int ng)
     return r;
 }
 
-// One tile of K (ISV false) or V: raw codes and scales -> f16 operand rows, and the tile's
-// per-token numbers: K the factor of a score; V log2 of the value scale and its inverse.
+// A token's numbers: of K the factor of a score, of V log2 of the value scale (NaN where the
+// row's values are not all numbers) and its inverse.
+template <int KIND, bool GRP, bool ISV>
+__device__ __forceinline__ void token_numbers(const uint16_t *sc, int t, bool bad, int nvalid, int ng, float tensor,
+                                              bool is_tensor, float *p0, float *p1)
+{
+    constexpr int PAIR = KIND == K_ASYM ? 2 : 1;
+    if constexpr (GRP) {
+        const RowScale r = row_scale<KIND>(sc, t, ng);
+        if constexpr (ISV) {
+            p0[t] = bad || r.bad ? __int_as_float(0x7fc00000) : (float)r.e;
+            p1[t] = pow2i(-r.e);
+        } else {
+            p0[t] = pow2i(r.e);
+        }
+    } else {
+        float s = 1.f;
+        if (KIND != K_F16) s = is_tensor ? tensor : __half2float(__ushort_as_half(sc[t * PAIR]));
+        if (KIND == K_ASYM) bad = bad || (sc[t * PAIR + 1] & 0x7fff) > 0x5bf8;
+        if constexpr (ISV) {
+            s = fabsf(s);
+            if (!(s < INFINITY)) bad = true;
+            // every value of the row is zero, or nothing may come of it (the inverse meets
+            // P = 0 where the token is masked, so it has to be a number)
+            if (s == 0.f || bad || t >= nvalid) s = 1.f;
+            p0[t] = bad ? __int_as_float(0x7fc00000) : lg2(s);
+            p1[t] = __fdividef(1.f, s);
+        } else {
+            p0[t] = s;
+        }
+    }
+}
+
+// One tile of K (ISV false) or V: raw codes and scales -> f16 operand rows.
 // Rows past nvalid of V are zeros (P is zero there, and stale bytes must not be NaN).
 template <int DH, int KIND, bool GRP, bool ISV>
 __device__ __forceinline__ void convert(const uint8_t *raw, const uint16_t *sc, uint8_t *dst, uint32_t lo_off,
@@ -347,38 +390,10 @@ __device__ __forceinline__ void convert(const uint8_t *raw, const uint16_t *sc, 
     const int c = ct & 7, tr = ct >> 3, lane = ct & 31;
     const int turn = KIND == K_INT4 ? (tr >> 1) & 1 : tr & 1;
 
-    auto params = [&](int t, bool bad) {
-        if constexpr (GRP) {
-            const RowScale r = row_scale<KIND>(sc, t, ng);
-            if constexpr (ISV) {
-                p0[t] = bad || r.bad ? __int_as_float(0x7fc00000) : (float)r.e;
-                p1[t] = pow2i(-r.e);
-            } else {
-                p0[t] = pow2i(r.e);
-            }
-        } else {
-            float s = 1.f;
-            if (KIND != K_F16) s = is_tensor ? tensor : __half2float(__ushort_as_half(sc[t * PAIR]));
-            if (KIND == K_ASYM) bad = bad || (sc[t * PAIR + 1] & 0x7fff) > 0x5bf8;
-            if constexpr (ISV) {
-                s = fabsf(s);
-                if (!(s < INFINITY)) bad = true;
-                // every value of the row is zero, or nothing may come of it (the inverse meets
-                // P = 0 where the token is masked, so it has to be a number)
-                if (s == 0.f || bad || t >= nvalid) s = 1.f;
-                p0[t] = bad ? __int_as_float(0x7fc00000) : lg2(s);
-                p1[t] = __fdividef(1.f, s);
-            } else {
-                p0[t] = s;
-            }
-        }
-    };
-    if (!CHECK) params(ct, false);                             // a thread a token
-
     const uint8_t *src = raw + tr * ROW + c * Raw<KIND>::BYTES;
     uint8_t *out = dst + tr * 128 + ((c ^ tr) & 7) * 16;      // (t ^ tr) & 7 = 0: RPP is a multiple of 8
     uint32_t bad_rows = 0;                                     // CHECK: bit u for pass u
-#pragma unroll
+#pragma unroll 1
     for (int pn = 0; pn < PANELS; pn++) {
         const int panel = PANELS == 2 ? pn ^ turn : 0;
         const int g = (c * 8 + 64 * panel) >> gshift;
@@ -427,7 +442,8 @@ __device__ __forceinline__ void convert(const uint8_t *raw, const uint16_t *sc, 
     }
     if (CHECK && c == 0)
 #pragma unroll 1
-        for (int u = 0; u < PASSES; u++) params(u * RPP + tr, (bad_rows >> u) & 1u);
+        for (int u = 0; u < PASSES; u++)
+            token_numbers<KIND, GRP, ISV>(sc, u * RPP + tr, (bad_rows >> u) & 1u, nvalid, ng, tensor, is_tensor, p0, p1);
     if (__builtin_expect(ISV && nvalid < TT, 0)) {
         // the last tile: zeros past the sequence's end
         const uint4 none = make_uint4(0u, 0u, 0u, 0u);
@@ -458,6 +474,7 @@ __device__ __forceinline__ bool convert_tiles(const TreeParams &p, const Work &w
     const uint32_t tile_bytes = keep(ISV ? p.l.v_bytes : p.l.k_bytes), entry_bytes = keep(p.l.entry_bytes);
     const uint32_t off_scales = keep(p.l.off_scales), lo = keep(p.l.lo);
     uint64_t *ready = ISV ? ctl->pready : ctl->sready, *used = ISV ? ctl->pvdone : ctl->sfull;
+    constexpr bool CHECK = ISV && (KIND == K_E4M3 || KIND == K_F16);   // numbers after the conversion
     int s = ISV, use = 0, i = 0;
     Walk it;
 #pragma unroll 1
@@ -465,21 +482,28 @@ __device__ __forceinline__ bool convert_tiles(const TreeParams &p, const Work &w
         int left = it.s.total - it.tile * TT;
 #pragma unroll 1
         for (int k = it.count; k > 0; k--, i++, left -= TT) {
-            if (!wait_warp(&ctl->full[s], use, abort_flag, limit)) return false;
-            // the operand's last use: S, or P V, of tile i - bufs
-            if (i >= bufs && !wait_warp(&used[(i - bufs) & 1], (i - bufs) >> 1, abort_flag, limit)) return false;
+            if (!wait_warp<kLongNap>(&ctl->full[s], use, abort_flag, limit)) return false;
             const uint8_t *entry = smem + (uint32_t)s * entry_bytes;
-            const int buf = i & (bufs - 1);
-            convert<DH, KIND, GRP, ISV>(entry, reinterpret_cast<const uint16_t *>(entry + off_scales),
-                                        tiles + (uint32_t)buf * tile_bytes, lo, min(TT, left), ct, ng, gshift, tensor,
-                                        is_tensor, ISV ? par->lv[i & 3] : par->sk[i & 3], par->iv[i & 3]);
+            const uint16_t *sc = reinterpret_cast<const uint16_t *>(entry + off_scales);
+            float *p0 = ISV ? par->lv[i & 3] : par->sk[i & 3], *p1 = par->iv[i & 3];
+            if (ISV && !CHECK) {
+                // V's numbers before its buffer is free: the softmax wants them that much earlier
+                // (slot i & 3 was last read for tile i - 4, whose P V is done)
+                token_numbers<KIND, GRP, ISV>(sc, ct, false, min(TT, left), ng, tensor, is_tensor, p0, p1);
+                __syncwarp();
+                mbar_arrive_if(&ctl->par[i & 3], (ct & 31) == 0);
+            }
+            // the operand's last use: S, or P V, of tile i - bufs
+            if (i >= bufs && !wait_warp<kLongNap>(&used[(i - bufs) & 1], (i - bufs) >> 1, abort_flag, limit)) return false;
+            // (S of tile i - 2 is done, so that its group has read the numbers of tile i - 4)
+            if (!ISV) token_numbers<KIND, GRP, ISV>(sc, ct, false, min(TT, left), ng, tensor, is_tensor, p0, p1);
+            convert<DH, KIND, GRP, ISV>(entry, sc, tiles + (uint32_t)(i & (bufs - 1)) * tile_bytes, lo, min(TT, left), ct, ng,
+                                        gshift, tensor, is_tensor, p0, p1);
             fence_proxy_async_shared();
             __syncwarp();
-            if ((ct & 31) == 0) {
-                mbar_arrive(&ctl->par[i & 3]);       // before the tile can be used, so that its
-                mbar_arrive(&ready[i & 1]);          // phase is over when the slot comes round
-                mbar_arrive(&ctl->empty[s]);
-            }
+            if (CHECK) mbar_arrive_if(&ctl->par[i & 3], (ct & 31) == 0);
+            mbar_arrive_if(&ready[i & 1], (ct & 31) == 0);
+            mbar_arrive_if(&ctl->empty[s], (ct & 31) == 0);
             s += 2;
             if (s >= E) {
                 s -= E;
@@ -608,8 +632,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         *static_cast<volatile int *>(abort_flag) = 1;
         atomicExch(p.status, KVQ_ERR_TIMEOUT);
     };
-    auto wait1 = [&](uint64_t *bar, int parity) { return wait_bounded(bar, parity, abort_flag, limit); };
-    auto wait = [&](uint64_t *bar, int parity) { return wait_warp(bar, parity, abort_flag, limit); };
+    auto wait1 = [&](uint64_t *bar, int parity) { return wait_bounded<kShortNap>(bar, parity, abort_flag, limit); };
+    auto wait = [&](uint64_t *bar, int parity) { return wait_warp<kShortNap>(bar, parity, abort_flag, limit); };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < E; s++) {
@@ -617,16 +641,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             mbar_init(&ctl->empty[s], kConvWarps / 2);
         }
         for (int j = 0; j < 2; j++) {
-            mbar_init(&ctl->sready[j], kConvWarps / 2 + 2 * kSoftWarps);
+            mbar_init(&ctl->sready[j], kConvWarps / 2 + kSoftWarps);
             mbar_init(&ctl->sfull[j], 1);
-            mbar_init(&ctl->pready[j], kConvWarps / 2 + 2 * kSoftWarps);
+            mbar_init(&ctl->pready[j], kConvWarps / 2 + kSoftWarps);
             mbar_init(&ctl->pvdone[j], 1);
         }
-        for (int j = 0; j < 4; j++) mbar_init(&ctl->par[j], kConvWarps);
+        for (int j = 0; j < 4; j++) mbar_init(&ctl->par[j], kConvWarps / 2);
         mbar_init(&ctl->drain, 1);
         ctl->abort = 0;
         fence_mbar_init();
     }
+    if (threadIdx.x < TT) ctl->m[threadIdx.x] = -INFINITY;
     if (warp == kMmaWarp) {
         tmem_alloc(&ctl->tmem, 512);
         tmem_relinquish();
@@ -647,48 +672,43 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     if (warp < 2 * kSoftWarps) {
         more_regs<kSoftRegs>();
         // ====================== softmax ======================
-        // two groups of four warps: group g takes tokens 64 g .. 64 g + 63 of every tile, with
-        // an O of its own
+        // two groups of four warps take the tiles in turns (a tile's scores are in the S of its
+        // parity); O, and the m that it is scaled by, are common to both
         const int grp = warp / kSoftWarps;
         const int place = threadIdx.x & (TT - 1);    // TMEM lane
         const uint32_t lane_off = (uint32_t)(place & ~31) << 16;
-        const uint32_t s_at = tmem + COL_S + 64u * grp + lane_off, o_at = tmem + COL_O + 128u * grp + lane_off;
+        const uint32_t s_row = tmem + COL_S + 128u * grp + lane_off, o_row = tmem + COL_O + lane_off;
+        const uint32_t p_row = over ? s_row : tmem + COL_P + lane_off;
         float *stage = reinterpret_cast<float *>(smem + keep(p.l.off_stage));
         const float osign = p.fmt == KVQ_FMT_TENSOR && __half2float(p.v.scales[0]) < 0.f ? -1.f : 1.f;
-        const uint32_t p_row = over ? s_at : tmem + COL_P + 32u * grp + lane_off;
         // A wait that gave up does not end the role: the eight warps meet at a hardware barrier
         // at every segment's end, so all of them walk on to the end (with the abort flag up no
         // further wait takes time) and write nothing more.
         bool ok = true;
         auto hold = [&](uint64_t *bar, int parity) {
-            if (!wait(bar, parity) && ok) {
-                ok = false;
-                give_up();
-            }
+            if (__builtin_expect(!mbar_try_wait(bar, parity & 1), 0))
+                if (!wait1(bar, parity) && ok) {
+                    ok = false;
+                    give_up();
+                }
+            __syncwarp();
         };
         auto soft_sync = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(64 * kSoftWarps) : "memory"); };
-        auto blank = [&](uint32_t at, int tb, int chunks) {
-            uint32_t none[8];
-#pragma unroll
-            for (int x = 0; x < 8; x++) none[x] = 0u;
-#pragma unroll 1
-            for (int c = chunks; c < 4; c++) tmem_st8(at + (((uint32_t)tb / 2 + 8u * c) & 31u), none);
-        };
         // What a thread keeps of its row; the next segment's is made while the last tile of the
         // current one is with the tensor cores.
         struct Row {
-            int rows, copies, tb;                    // rows of the tile, their copies; first of the group's
-                                                     // tokens that this copy takes
+            int rows, copies, tb;                    // rows of the tile, their copies; first token of a tile
+                                                     // that this copy takes
             float rf;                                // factor of a score: tau log2(e), the query's power of two
             uint64_t mask;                           // drafted tokens that the row attends
         };
-        // this thread's row of the walk's segment, its query into TMEM
-        auto open = [&](const Walk &o) {
+        // this thread's row of the walk's segment; store: its query into TMEM
+        auto open = [&](const Walk &o, bool store) {
             Row x;
             x.rows = min(kTreeRows, o.s.n * p.G - o.rt * kTreeRows);
             x.copies = x.rows <= 32 ? 4 : x.rows <= 64 ? 2 : 1;
             const int r = place & (TT / x.copies - 1);
-            x.tb = (place - r) / 2;
+            x.tb = place - r;
             const int rr = o.rt * kTreeRows + r, qi = rr / p.G;
             const bool live = r < x.rows;
             const int64_t at = (((int64_t)o.b * p.n_tree + qi) * p.n_q_heads + (int64_t)o.head * p.G + rr - qi * p.G) * DH;
@@ -707,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 x.rf = p.tau_log2e * pow2i(ex);
                 return pow2i(-ex);
             };
-            if (p.q_dtype == KVQ_F16 && grp == 1) return x;
+            if (p.q_dtype == KVQ_F16 && !store) return x;
             if (p.q_dtype != KVQ_F32) {
                 // the whole row at once, one wait for memory
                 uint4 u[DH / 8];
@@ -724,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                         low = max(low, h[k] & 0x00007fffu);
                     }
                     const float pre = level(__uint_as_float(max(top, low << 16)));
-                    if (grp == 1) return x;
+                    if (!store) return x;
 #pragma unroll
                     for (int k = 0; k < DH / 2; k++)
                         h[k] = pack_half2(__uint_as_float(h[k] << 16) * pre, __uint_as_float(h[k] & 0xffff0000u) * pre);
@@ -742,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                     a = fmaxf(fmaxf(a, fmaxf(fabsf(f.x), fabsf(f.y))), fmaxf(fabsf(f.z), fabsf(f.w)));
                 }
                 const float pre = level(a);
-                if (grp == 1) return x;
+                if (!store) return x;
 #pragma unroll 1
                 for (int c = 0; c < DH / 32; c++) {
                     uint32_t hi[16], lo[16];
@@ -765,173 +785,212 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         };
         Walk it;
         Row row{};
+        float m = -INFINITY, l = 0.f;                // the group's: l in units of 2^m
         int i = 0;                                   // units done
+        // P of tile i, CH times 32 tokens a thread.
+        // The probabilities are made in registers, with the m that stands when the tile begins.
+        // P's columns are free, and m is final up to this tile, once P V of the tile before is
+        // done: then P goes out, scaled again if the other group has raised m meanwhile.
+        // m is raised in a second pass over the tile, when some token would not fit; O is then
+        // rescaled between the two tiles' P V, with no other P in flight.
+        auto tiles = [&](auto ch, int i0, int count) {
+            constexpr int CH = decltype(ch)::value, N = CH == 4 ? 16 : 32;   // (tokens at a time: registers)
+#pragma unroll 1
+            for (int k = (i0 ^ grp) & 1; k < count; k += 2) {
+                i = i0 + k;
+                const int j = i & 1;                     // == grp
+                const float *sk = par->sk[i & 3] + row.tb, *lv = par->lv[i & 3] + row.tb, *iv = par->iv[i & 3] + row.tb;
+                const int t0 = (it.tile + k) * TT + row.tb;
+                const bool whole = t0 + 32 * CH <= it.s.len;
+                const uint32_t s_at = s_row + (uint32_t)row.tb, p_at = p_row + (uint32_t)row.tb / 2;
+                uint32_t pw[CH][16];
+                float sum;
+                const float now = ctl->m[place];
+                if (now != m) {
+                    l *= ex2(m - now);
+                    m = now;
+                }
+                hold(&ctl->sfull[j], i >> 1);
+                hold(&ctl->par[i & 3], i >> 2);
+                tc_fence_after();
+#pragma unroll 1
+                for (bool second = false;; second = true) {
+                    bool fits = true;
+                    sum = 0.f;
+                    const float me = m == -INFINITY ? 0.f : m;
+#pragma unroll
+                    for (int c = 0; c < 32 * CH; c += N) {
+                        uint32_t a[N];
+                        uint64_t z[N / 2];
+                        tmem_ld_async(s_at + c, a);
+                        tmem_ld_wait(a);
+                        const uint32_t vis = whole ? FULL : visible(t0 + c, it.s.len, row.mask) | (N == 32 ? 0u : 0xffff0000u);
+                        const float mx = scores<N>(a, sk + c, lv + c, row.rf, vis, z);
+                        fits = fits && (!(mx > m + kMoveAt) || mx == -INFINITY);
+                        sum += probs<N>(z, iv + c, me, *reinterpret_cast<uint32_t(*)[N / 2]>(&pw[0][0] + c / 2));
+                    }
+                    if (second || __builtin_expect(__all_sync(FULL, fits), 1)) break;
+                    // ---- the tile's maximum, then m, O and l after it
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < 32 * CH; c += 16) {
+                        uint32_t a[16];
+                        uint64_t z[8];
+                        tmem_ld_async(s_at + c, a);
+                        tmem_ld_wait(a);
+                        const uint32_t vis = whole ? FULL : visible(t0 + c, it.s.len, row.mask) | 0xffff0000u;
+                        top = fmaxf(top, scores<16>(a, sk + c, lv + c, row.rf, vis, z));
+                    }
+                    if (k > 0) hold(&ctl->pvdone[j ^ 1], (i - 1) >> 1);
+                    tc_fence_after();
+                    const float was = ctl->m[place];
+                    const bool set = was == -INFINITY && top > -INFINITY, up = !set && top > was + kMoveAt;
+                    const float to = set || up ? floorf(top) - kHead : was;
+                    const float alpha = up ? ex2(was - to) : 1.f;     // both whole: a power of two
+                    if (__any_sync(FULL, up)) {
+#pragma unroll 1
+                        for (int q = 0; q < DH; q += 16) {
+                            uint32_t x[16];
+                            tmem_ld16(o_row + q, x);
+#pragma unroll
+                            for (int y = 0; y < 16; y++) x[y] = __float_as_uint(__uint_as_float(x[y]) * alpha);
+                            tmem_st16(o_row + q, x);
+                        }
+                    }
+                    ctl->m[place] = to;
+                    if (to != m) {
+                        l *= ex2(m - to);
+                        m = to;
+                    }
+                }
+                l += sum;
+                // the scores are read: those of two tiles on may come
+                if (!over && k + 2 < count) {
+                    tc_fence_before();
+                    __syncwarp();
+                    mbar_arrive_if(&ctl->sready[j], lane == 0);
+                }
+                if (k > 0) hold(&ctl->pvdone[j ^ 1], (i - 1) >> 1);
+                tc_fence_after();
+                const float then = ctl->m[place];
+                if (__builtin_expect(__any_sync(FULL, then != m), 0)) {
+                    const float alpha = m == then ? 1.f : ex2(m - then);
+                    const uint32_t alpha2 = pack_half2(alpha, alpha);
+                    l *= alpha;
+                    m = then;
+#pragma unroll
+                    for (int c = 0; c < CH; c++)
+#pragma unroll
+                        for (int q = 0; q < 16; q++) pw[c][q] = hmul2_u32(pw[c][q], alpha2);
+                }
+#pragma unroll
+                for (int c = 0; c < CH; c++) tmem_st16(p_at + 16u * c, pw[c]);
+                if (CH < 4 && (over || k == 0)) {
+                    // zeros for the other copies' tokens: scores left theirs, or the tile is the first
+                    uint32_t none[16];
+#pragma unroll
+                    for (int x = 0; x < 16; x++) none[x] = 0u;
+#pragma unroll 1
+                    for (int c = CH; c < 4; c++) tmem_st16(p_row + (((uint32_t)row.tb / 2 + 16u * c) & 63u), none);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                mbar_arrive_if(&ctl->pready[j], lane == 0);
+                if (over && k + 2 < count) mbar_arrive_if(&ctl->sready[j], lane == 0);
+            }
+        };
         // segment by segment; a first pass without tiles only opens the first one
         it.start(p, w);
         bool opened = false;
 #pragma unroll 1
         while (it.count) {
-            float m = -INFINITY, l = 0.f;
-            const int i0 = i, copies = row.copies, tb = row.tb, count = opened ? it.count : 0;
-#pragma unroll 1
-            for (int k = 0; k < count; k++, i++) {
-                // ---- P of this thread's tokens, over the columns of their scores
-                const int j = i & 1;
-                hold(&ctl->sfull[j], i >> 1);
-                tc_fence_after();
-                const int at = HT * grp + tb;
-                const float *sk = par->sk[i & 3] + at, *lv = par->lv[i & 3] + at, *iv = par->iv[i & 3] + at;
-                const int t0 = (it.tile + k) * TT + HT * grp;
-                const bool whole = t0 + HT <= it.s.len;
-                const uint32_t p_at = p_row + (uint32_t)tb / 2;
-                // raise m to fit a maximum
-                auto fit = [&](float mx, int c) {
-                    const bool set = m == -INFINITY && mx > -INFINITY, up = !set && mx > m + kMoveAt;
-                    float alpha = 1.f;
-                    if (set || up) {
-                        const float to = floorf(mx) - kHead;
-                        if (up) alpha = ex2(m - to);             // m and to are whole: a power of two
-                        m = to;
-                        l *= alpha;
-                    }
-                    if (__builtin_expect(!__any_sync(FULL, up), 1)) return;
-                    // m moved too far for some row: O follows (every P V before this tile is in
-                    // it; in a segment's first tile there is nothing yet), and this tile's P
-                    uint32_t x[16];
-                    if (k > 0) {
-                        hold(&ctl->pvdone[j ^ 1], (i - 1) >> 1);
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int q = 0; q < DH / 16; q++) {
-                            tmem_ld16(o_at + 16u * q, x);
-#pragma unroll
-                            for (int y = 0; y < 16; y++) x[y] = __float_as_uint(__uint_as_float(x[y]) * alpha);
-                            tmem_st16(o_at + 16u * q, x);
-                        }
-                    }
-                    const uint32_t alpha2 = pack_half2(alpha, alpha);
-#pragma unroll 1
-                    for (int n = 0; n < c; n++) {
-                        uint32_t y[8];
-                        tmem_st_wait();
-                        tmem_ld8(p_at + 8u * n, y);
-#pragma unroll
-                        for (int q = 0; q < 8; q++) y[q] = hmul2_u32(y[q], alpha2);
-                        tmem_st8(p_at + 8u * n, y);
-                    }
-                };
-                // N tokens from chunk c on: P over the columns of scores that are read (it takes half
-                // as many), or of the P before, which its product has to be done with
-                auto chunk = [&](auto n, int c, bool done) {
-                    constexpr int N = decltype(n)::value;
-                    uint32_t a[N], pw[N / 2];
-                    uint64_t z[N / 2];
-                    tmem_ld_async(s_at + tb + N * c, a);
-                    if (c == 0) hold(&ctl->par[i & 3], i >> 2);
-                    tmem_ld_wait(a);
-                    const int tok = t0 + tb + N * c;
-                    uint32_t vis = FULL;
-                    if (!whole) vis = visible(tok, it.s.len, row.mask) | (N == 32 ? 0u : 0xffff0000u);
-                    const float mx = scores<N>(a, sk + N * c, lv + N * c, row.rf, vis, z);
-                    if (done && !over && k + 1 < count) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&ctl->sready[j ^ 1]);
-                    }
-                    fit(mx, N / 16 * c);
-                    l += probs<N>(z, iv + N * c, m == -INFINITY ? 0.f : m, pw);
-                    if (c == 0 && k > 0 && !over) {
-                        hold(&ctl->pvdone[j ^ 1], (i - 1) >> 1);
-                        tc_fence_after();
-                    }
-                    tmem_st_cols(p_at + N / 2 * c, pw);
-                };
-                if (copies == 4) {
-                    chunk(Int<16>(), 0, true);
-                } else {
-#pragma unroll 1
-                    for (int c = 0; c < 2 / copies; c++) chunk(Int<32>(), c, c == 2 / copies - 1);
-                }
-                // zeros for the other copies' tokens: scores left theirs, or they are there already
-                if (copies > 1 && (over || k == 0)) blank(p_row, tb, 4 / copies);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&ctl->pready[j]);
-                    if (over && k + 1 < count) mbar_arrive(&ctl->sready[j ^ 1]);
-                }
-            }
-            // ---- the next segment's queries come in: this one's scores are all done
+            const int i0 = i, copies = row.copies, count = opened ? it.count : 0;
+            if (copies == 4)
+                tiles(Int<1>(), i0, count);
+            else if (copies == 2)
+                tiles(Int<2>(), i0, count);
+            else
+                tiles(Int<4>(), i0, count);
+            i = i0 + count;
+            // ---- the next segment's queries come in, by the group of its first tile, once this
+            // one's scores are all done; the other group has read its S
             const int last = i - 1;
             Walk ahead = it;
             if (opened) ahead.next(p);
             Row next{};
             if (ahead.count) {
-                next = open(ahead);
+                const bool mine = (i & 1) == grp;
+                if (mine && opened) {
+                    hold(&ctl->sfull[last & 1], last >> 1);
+                    tc_fence_after();
+                }
+                next = open(ahead, mine);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->sready[i & 1]);
+                if (mine || ahead.count > 1) mbar_arrive_if(&ctl->sready[grp], lane == 0);
             }
             if (!opened) {
                 opened = true;
                 row = next;
                 continue;
             }
-            // join the groups and copies of every row; the output, or a partial
+            // ---- join the groups' sums and the copies of every row; the output, or a partial
             const int nr = TT / copies, r = place & (nr - 1), rows = row.rows;
             ctl->ml[grp][place] = make_float2(m, l);
+            hold(&ctl->pvdone[last & 1], last >> 1);
+            tc_fence_after();
             soft_sync();
             float M = -INFINITY, L = 0.f;
 #pragma unroll 1
-            for (int c = r; c < 2 * TT; c += nr) M = fmaxf(M, ctl->ml[0][c].x);
+            for (int c = r; c < TT; c += nr) M = fmaxf(M, ctl->m[c]);
 #pragma unroll 1
             for (int c = r; c < 2 * TT; c += nr) {
                 const float2 x = ctl->ml[0][c];
                 L += x.x == -INFINITY ? 0.f : x.y * ex2(x.x - M);
             }
+            const float mine = ctl->m[place];
+            float f = mine == -INFINITY ? 0.f : ex2(mine - M) * osign;
             const long long u0 = w.u0 + i0 - it.tile, u1 = u0 + it.s.tiles;
             const bool opens = u0 >= w.u0, direct = opens && u1 <= w.u0 + n_units;
             // a CTA leaves two partials at most: of its first segment, and of its last
             const int slot = 2 * (int)blockIdx.x + (i0 == 0 ? 0 : 1);
             float *part = p.slots + (int64_t)slot * tree_slot_floats(p.slot_rows, DH);
-            float f = m == -INFINITY ? 0.f : ex2(m - M) * osign;
             if (direct) f = L != 0.f ? f / L : 0.f;
             if (threadIdx.x == 0 && opens && ok)
                 p.seg[((int64_t)it.b * p.rows.heads + it.head) * p.row_tiles + it.rt] =
                     make_int4(slot, blockIdx.x, direct ? 1 : range_cta(u1 - 1, w.n, w.p) - (int)blockIdx.x + 1, 0);
-            if (!direct && threadIdx.x < rows)
+            if (!direct && ok && threadIdx.x < rows)
                 *reinterpret_cast<float2 *>(part + (int64_t)p.slot_rows * DH + 2 * place) = make_float2(M, L);
-            hold(&ctl->pvdone[last & 1], last >> 1);
-            tc_fence_after();
-            // four columns of a row a thread: rows threadIdx.x / 4 and, of more than 64, + 64
-            const int r0 = threadIdx.x >> 2, col = (threadIdx.x & 3) * 4;
-            const int64_t out0 = ((int64_t)it.b * p.n_tree * p.n_q_heads + (int64_t)it.head * p.G) * DH + col;
+            // 32 columns of O a round, 16 by each group; then eight lanes a row, four columns each
+            const int r0 = threadIdx.x >> 3, half = (threadIdx.x >> 2) & 1, col = (threadIdx.x & 3) * 4;
+            const int64_t out0 = ((int64_t)it.b * p.n_tree * p.n_q_heads + (int64_t)it.head * p.G) * DH;
 #pragma unroll 1
-            for (int c = 0; c < DH / 16; c++) {
+            for (int c = 0; c < DH; c += 32) {
                 uint32_t o[16];
-                tmem_ld16(o_at + 16u * c, o);
+                tmem_ld16(o_row + c + 16u * grp, o);
                 if (c > 0) soft_sync();                              // the staging was read
 #pragma unroll
                 for (int x = 0; x < 16; x++)
                     stage[(grp * TT + place) * STAGE_LD + x] = f == 0.f ? 0.f : __uint_as_float(o[x]) * f;
                 soft_sync();
+                if (c == 0 && grp == 0) ctl->m[place] = -INFINITY;   // for the next segment
 #pragma unroll 1
-                for (int k = 0; k < 2 && ok; k++) {
-                    const int rr = r0 + 64 * k;
-                    if (rr >= rows) break;
+                for (int rr = r0; rr < rows && ok; rr += 32) {
                     float y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-                    for (int q = rr; q < 2 * TT; q += nr)
+                    for (int q = rr; q < TT; q += nr)
 #pragma unroll
-                        for (int d = 0; d < 4; d++) y[d] += stage[q * STAGE_LD + col + d];
-                    const int gr = it.rt * kTreeRows + rr, qi = gr / p.G;
+                        for (int d = 0; d < 4; d++) y[d] += stage[(half * TT + q) * STAGE_LD + col + d];
+                    const int gr = it.rt * kTreeRows + rr, qi = gr / p.G, at = c + 16 * half + col;
                     if (direct)
-                        store4(p.out, out0 + ((int64_t)qi * (p.n_q_heads - p.G) + gr) * DH + 16 * c, p.out_dtype, y);
+                        store4(p.out, out0 + ((int64_t)qi * (p.n_q_heads - p.G) + gr) * DH + at, p.out_dtype, y);
                     else
-                        *reinterpret_cast<float4 *>(part + rr * DH + col + 16 * c) = make_float4(y[0], y[1], y[2], y[3]);
+                        *reinterpret_cast<float4 *>(part + rr * DH + at) = make_float4(y[0], y[1], y[2], y[3]);
                 }
             }
+            m = -INFINITY;
+            l = 0.f;
             row = next;
             it = ahead;
         }
@@ -972,7 +1031,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                     const int nsc = (nv + 7) & ~7;      // rows whose scales are whole 16-byte pieces
 #pragma unroll 1
                     for (int kv = 0; kv < 2; kv++, e++) {
-                        if (use > 0 && !(ok = wait1(&ctl->empty[s], use - 1))) break;
+                        if (use > 0 && !(ok = wait_bounded<kLongNap>(&ctl->empty[s], use - 1, abort_flag, limit))) break;
                         const CacheTensor &ten = kv ? p.v : p.k;
                         const int rb = kv ? vr : kr, sb = kv ? vsb : ksb;
                         uint8_t *dst = smem + (uint32_t)s * p.l.entry_bytes;
@@ -1002,7 +1061,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             const uint64_t k_desc = sw128_desc(sbase + keep(p.l.off_k)), v_desc = sw128_mn_desc(sbase + keep(p.l.off_v), PANEL, 1024u);
             // (descriptors count 16-byte units)
             const uint32_t lo = keep(p.l.lo) >> 4, k_step = keep(p.l.k_bytes) >> 4, v_step = keep(p.l.v_bytes) >> 4;
-            const uint32_t p_col = over ? COL_S : COL_P, p_gap = over ? 32u : 0u;   // P, and what lies between the halves
             const int q_parts = over ? 2 : 1, s_parts = (1 + keep(p.l.k_grouped)) * q_parts, v_parts = 1 + keep(p.l.v_grouped);
             // scores of tile i
             auto issue_s = [&](int i) {
@@ -1012,29 +1070,30 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 for (int part = 0; part < s_parts; part++) {
                     const int kp = q_parts == 2 ? part >> 1 : part, qp = q_parts == 2 ? part & 1 : 0;
                     const uint64_t d = k_desc + ((i & (KB - 1)) * k_step + kp * lo);
-                    const uint32_t qa = tm + (qp ? COL_QLO : COL_Q);
+                    const uint32_t qa = tm + (qp ? COL_QLO : COL_Q), st = tm + COL_S + 128u * (i & 1);
                     if (leader)
 #pragma unroll
                         for (int kk = 0; kk < DH / 16; kk++)
-                            umma_f16_ts(tm + COL_S, qa + 8u * kk, d + ((kk >> 2) * (PANEL >> 4) + 2u * (kk & 3)), IDESC_S,
+                            umma_f16_ts(st, qa + 8u * kk, d + ((kk >> 2) * (PANEL >> 4) + 2u * (kk & 3)), IDESC_S,
                                         kk > 0 ? 1u : (uint32_t)(part > 0));
                 }
                 if (leader) umma_commit(&ctl->sfull[i & 1]);
                 __syncwarp();
                 return true;
             };
-            // O += P V of tile i: each softmax group's half of the tokens into its own O
+            // O += P V of tile i
             auto issue_pv = [&](int i, bool first) {
                 if (!wait(&ctl->pready[i & 1], i >> 1)) return false;
                 tc_fence_after();
 #pragma unroll 1
                 for (int part = 0; part < v_parts; part++) {
                     const uint64_t d = v_desc + ((i & (VB - 1)) * v_step + part * lo);
+                    const uint32_t pa = tm + (over ? COL_S + 128u * (i & 1) : COL_P);
                     if (leader)
 #pragma unroll
                         for (int kk = 0; kk < TT / 16; kk++)
-                            umma_f16_ts(tm + COL_O + (kk < 4 ? 0u : 128u), tm + p_col + 8u * kk + (kk < 4 ? 0u : p_gap),
-                                        d + 128u * kk, IDESC_O, (kk & 3) > 0 ? 1u : (uint32_t)(!first || part > 0));
+                            umma_f16_ts(tm + COL_O, pa + 8u * kk, d + 128u * kk, IDESC_O,
+                                        kk > 0 ? 1u : (uint32_t)(!first || part > 0));
                 }
                 if (leader) umma_commit(&ctl->pvdone[i & 1]);
                 __syncwarp();
@@ -1046,14 +1105,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 #pragma unroll 1
             for (it.start(p, w); it.count && ok; it.next(p)) {
                 const int count = __shfl_sync(FULL, it.count, 0);
-                ok = issue_s(i);
+                ok = issue_s(i) && (count < 2 || issue_s(i + 1));
 #pragma unroll 1
                 for (int k = 0; k < count && ok; k++, i++) {
-                    // the next tile's scores go first, unless this one's P lies over them
-                    const bool more = k + 1 < count;
-                    if (more && !over) ok = issue_s(i + 1);
+                    // scores two tiles ahead, over those that are read: before this tile's P V,
+                    // unless its P lies there
+                    const bool more = k + 2 < count;
+                    if (more && !over) ok = issue_s(i + 2);
                     ok = ok && issue_pv(i, k == 0);
-                    if (more && over) ok = ok && issue_s(i + 1);
+                    if (more && over) ok = ok && issue_s(i + 2);
                 }
             }
             if (!ok) give_up();
