@@ -47,6 +47,26 @@ __host__ __device__ inline int cache_slot(int t, int window, int n_anchor)
 
 cudaError_t launch_append(const AppendParams &k, const AppendParams *v, cudaStream_t stream);
 
+// Launch with programmatic stream serialisation: the kernel may be scheduled while the work
+// before it drains, and calls grid_dependency_wait() before it touches global memory.
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*fn)(P...), unsigned blocks, unsigned threads, size_t smem, cudaStream_t stream,
+                             A &&...args)
+{
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(blocks);
+    lc.blockDim = dim3(threads);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = stream;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    (void)cudaGetLastError();  // drop a stale, already-reported error of an earlier call
+    return cudaLaunchKernelEx(&lc, fn, static_cast<A &&>(args)...);
+}
+
 // ------------------------------------------------------------------ drafted tokens
 // Where a layer's rows lie: contiguous, ring or paged (pages of kPageTokens rows).
 struct CacheRows {

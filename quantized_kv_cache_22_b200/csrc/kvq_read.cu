@@ -9,50 +9,75 @@
 namespace kvq {
 namespace {
 
-// A thread turns eight neighbouring elements of a row into values: 16 lanes a 128-element
-// row, so that a warp's loads and stores are contiguous runs.  A block takes one head's
-// kReadTokens consecutive tokens of K or of V: its code reads are one contiguous range.
+// Memory-bound: bytes of codes and scales in, bytes of values out, nothing reused.  A thread
+// turns pieces of eight elements into values, sixteen (eight) lanes a row of 128 (64) elements,
+// so that a warp's loads and stores are whole runs of a row; it takes kReadUnroll rows at a
+// time, all their loads in flight first (one row a time left HBM at 2.7 TB/s).  A block takes
+// consecutive tokens of one head of K or of V, whose codes are one contiguous range.
+// Every code is exact in f16.  For F16 outputs the product with the scale is taken in f16:
+// rounded once from the exact product, it is what fp32 (exact) and a rounding would give.
 constexpr int kReadThreads = 256;
-constexpr int kReadUnroll = 4;
+constexpr int kReadUnroll = 8;
 
-template <int BITS>
+template <int KIND>
 __device__ __forceinline__ void read_rows(const ReadParams &p, const CacheTensor &t, const RowsView &out, int b,
                                           int head, int j0, int count, int first)
 {
-    const int chunks = p.dim / 8;                        // 8-element chunks of a row
-    const int per_pass = kReadThreads / min(chunks, kReadThreads);   // rows a pass handles
-    const int lane_row = threadIdx.x / min(chunks, kReadThreads);
+    const int chunks = p.dim / 8;                        // 8-element pieces of a row
+    const int lanes = min(chunks, kReadThreads);
+    const int per_pass = kReadThreads / lanes;           // rows a pass handles
+    const int lane_row = threadIdx.x / lanes;
     if (lane_row >= per_pass) return;
-    const int pairs = scale_vals(p.fmt);
-    for (int ch = threadIdx.x % min(chunks, kReadThreads); ch < chunks; ch += kReadThreads) {
-        int64_t row[kReadUnroll];
-        Codes8<BITS> code[kReadUnroll];
-        __half2 sc[kReadUnroll];
+    constexpr int PAIR = KIND == K_ASYM ? 2 : 1;
+    const bool tensor = p.fmt == KVQ_FMT_TENSOR;
+    const int ng = p.dim / t.group, gshift = t.group == 32 ? 5 : t.group == 64 ? 6 : 7;
+    const int64_t row_bytes = (int64_t)chunks * Raw<KIND>::BYTES;
+#pragma unroll 1
+    for (int ch = threadIdx.x % lanes; ch < chunks; ch += lanes) {
+        const int g = (ch * 8) >> gshift;
+        bool live[kReadUnroll];
+        Raw<KIND> raw[kReadUnroll];
+        uint32_t sc[kReadUnroll];                        // scale, zero-point << 16
 #pragma unroll
         for (int u = 0; u < kReadUnroll; u++) {
             const int j = j0 + u * per_pass + lane_row;
-            row[u] = j < count ? cache_row(p.rows, b, head, (int64_t)first + j) : -1;
-            if (row[u] < 0) continue;
-            code[u].load(t.codes + row[u] * ((int64_t)p.dim * BITS / 8), ch);
-            if constexpr (BITS != 16) {
-                const __half *s = p.fmt == KVQ_FMT_TENSOR
-                    ? t.scales : t.scales + (row[u] * (p.dim / t.group) + ch * 8 / t.group) * pairs;
-                sc[u] = __halves2half2(s[0], p.fmt == KVQ_FMT_ASYM ? s[1] : __ushort_as_half(0));
+            const int64_t row = j < count ? cache_row(p.rows, b, head, (int64_t)first + j) : -1;
+            live[u] = row >= 0;
+            sc[u] = 0x3c00u;
+            if (!live[u]) continue;
+            raw[u].w = __ldcs(reinterpret_cast<const decltype(raw[u].w) *>(t.codes + row * row_bytes + ch * Raw<KIND>::BYTES));
+            if constexpr (KIND != K_F16) {
+                const uint16_t *s = reinterpret_cast<const uint16_t *>(t.scales) + (tensor ? 0 : (row * ng + g) * PAIR);
+                sc[u] = KIND == K_ASYM ? *reinterpret_cast<const uint32_t *>(s) : *s;
             }
         }
 #pragma unroll
         for (int u = 0; u < kReadUnroll; u++) {
-            if (row[u] < 0) continue;
+            if (!live[u]) continue;
             const int j = j0 + u * per_pass + lane_row;
-            float x[8];
-            code[u].values(x, p.fmt);
-            if constexpr (BITS != 16) {
-                const float s = __low2float(sc[u]), z = __high2float(sc[u]);
+            uint32_t h[4];
+            uint32_t zero = 0u;
+            if constexpr (KIND == K_ASYM) zero = hadd2_u32((sc[u] >> 16) * 0x10001u, 0x64006400u);
+            codes_f16<KIND>(raw[u], zero, h);
+            const int64_t at = b * out.batch_stride + j * out.token_stride + (int64_t)head * p.dim + ch * 8;
+            if (p.out_dtype == KVQ_F16) {
+                if constexpr (KIND != K_F16) {
+                    const uint32_t s2 = (sc[u] & 0xffffu) * 0x10001u;
 #pragma unroll
-                for (int e = 0; e < 8; e++) x[e] = (p.fmt == KVQ_FMT_ASYM ? x[e] - z : x[e]) * s;
+                    for (int k = 0; k < 4; k++) h[k] = hmul2_u32(h[k], s2);
+                }
+                __stcs(reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out.data) + at), make_uint4(h[0], h[1], h[2], h[3]));
+                continue;
             }
-            store8(out.data, b * out.batch_stride + j * out.token_stride + (int64_t)head * p.dim + ch * 8,
-                   p.out_dtype, x);
+            const float s = KIND == K_F16 ? 1.f : __half2float(__ushort_as_half((unsigned short)sc[u]));
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const float2 v = unpack_half2(h[k]);
+                x[2 * k] = v.x * s;
+                x[2 * k + 1] = v.y * s;
+            }
+            store8(out.data, at, p.out_dtype, x);
         }
     }
 }
@@ -60,6 +85,8 @@ __device__ __forceinline__ void read_rows(const ReadParams &p, const CacheTensor
 __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constant__ ReadParams p, int tiles,
                                                             int tile_tokens)
 {
+    grid_dependency_wait();
+    grid_launch_dependents();
     int64_t i = blockIdx.x;
     const int tile = (int)(i % tiles);
     i /= tiles;
@@ -72,12 +99,13 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
     if (j0 >= count) return;
     const int first = p.d_pos[b];
     const CacheTensor &t = p.t[which];
-    if (t.bits == 8)
-        read_rows<8>(p, t, p.out[which], b, head, j0, count, first);
-    else if (t.bits == 4)
-        read_rows<4>(p, t, p.out[which], b, head, j0, count, first);
-    else
-        read_rows<16>(p, t, p.out[which], b, head, j0, count, first);
+    switch (kind_of(t.bits, p.fmt)) {
+    case K_INT8: return read_rows<K_INT8>(p, t, p.out[which], b, head, j0, count, first);
+    case K_INT4: return read_rows<K_INT4>(p, t, p.out[which], b, head, j0, count, first);
+    case K_E4M3: return read_rows<K_E4M3>(p, t, p.out[which], b, head, j0, count, first);
+    case K_ASYM: return read_rows<K_ASYM>(p, t, p.out[which], b, head, j0, count, first);
+    default: return read_rows<K_F16>(p, t, p.out[which], b, head, j0, count, first);
+    }
 }
 
 // One warp moves the path's rows of one (layer, sequence, head) of K or of V.  The path is
@@ -129,6 +157,8 @@ __device__ __forceinline__ void move_rows_any(uint8_t *base, int bytes, const Co
 
 __global__ void __launch_bounds__(256) commit_kernel(const __grid_constant__ CommitParams p)
 {
+    grid_dependency_wait();
+    grid_launch_dependents();
     const int lane = threadIdx.x & 31;
     int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int64_t total = (int64_t)p.n_layers * p.rows.batch * p.rows.heads * 2;
@@ -177,9 +207,7 @@ cudaError_t launch_read(const ReadParams &p, cudaStream_t stream)
     const int both = (p.out[0].data != nullptr) + (p.out[1].data != nullptr);
     const int64_t blocks = (int64_t)p.rows.batch * p.rows.heads * both * tiles;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    (void)cudaGetLastError();
-    read_kernel<<<(unsigned)blocks, kReadThreads, 0, stream>>>(p, tiles, tile_tokens);
-    return cudaGetLastError();
+    return launch_dependent(read_kernel, (unsigned)blocks, kReadThreads, 0, stream, p, tiles, tile_tokens);
 }
 
 cudaError_t launch_commit(const CommitParams &p, cudaStream_t stream)
@@ -187,9 +215,7 @@ cudaError_t launch_commit(const CommitParams &p, cudaStream_t stream)
     const int64_t warps = (int64_t)p.n_layers * p.rows.batch * p.rows.heads * 2;
     const int64_t blocks = (warps + 7) / 8;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    (void)cudaGetLastError();
-    commit_kernel<<<(unsigned)blocks, 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(commit_kernel, (unsigned)blocks, 256, 0, stream, p);
 }
 
 }  // namespace kvq

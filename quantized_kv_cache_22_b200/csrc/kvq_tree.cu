@@ -259,65 +259,6 @@ struct Walk {
 };
 
 // ------------------------------------------------------------------ codes to f16
-enum { K_INT8, K_INT4, K_E4M3, K_ASYM, K_F16 };
-
-__device__ __forceinline__ int kind_of(int bits, int fmt)
-{
-    return bits == 4 ? K_INT4 : bits == 16 ? K_F16 : fmt == KVQ_FMT_E4M3 ? K_E4M3 : fmt == KVQ_FMT_ASYM ? K_ASYM : K_INT8;
-}
-
-__device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ uint32_t hfma2_u32(uint32_t a, uint32_t b, uint32_t c)
-{
-    uint32_t r;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-    return r;
-}
-
-template <int KIND>
-struct Raw;
-template <> struct Raw<K_INT8> { uint2 w; static constexpr int BYTES = 8; };
-template <> struct Raw<K_ASYM> { uint2 w; static constexpr int BYTES = 8; };
-template <> struct Raw<K_E4M3> { uint2 w; static constexpr int BYTES = 8; };
-template <> struct Raw<K_INT4> { uint32_t w; static constexpr int BYTES = 4; };
-template <> struct Raw<K_F16> { uint4 w; static constexpr int BYTES = 16; };
-
-// Eight codes as f16, element pairs in the words' low and high halves.  Bytes become f16 by
-// putting them under the exponent of 1024 (0x64 in the high byte) and subtracting.
-template <int KIND>
-__device__ __forceinline__ void codes_f16(const Raw<KIND> &r, uint32_t zero, uint32_t (&h)[4])
-{
-    if constexpr (KIND == K_INT8 || KIND == K_ASYM) {
-        const uint32_t flip = KIND == K_INT8 ? 0x80808080u : 0u;
-        const uint32_t base = KIND == K_INT8 ? 0x64806480u : zero;   // 1024 + 128, or 1024 + zero-point
-        const uint32_t a = r.w.x ^ flip, b = r.w.y ^ flip;
-        h[0] = hsub2_u32(prmt(a, 0x64646464u, 0x4140), base);
-        h[1] = hsub2_u32(prmt(a, 0x64646464u, 0x4342), base);
-        h[2] = hsub2_u32(prmt(b, 0x64646464u, 0x4140), base);
-        h[3] = hsub2_u32(prmt(b, 0x64646464u, 0x4342), base);
-    } else if constexpr (KIND == K_INT4) {
-        // byte k twice; the low nibble stays (1024 + n), the high one is at 16 n (1024 + 16 n);
-        // the flipped sign bit adds 8 to each, and the multiply-add removes offset and factor
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-            const uint32_t x = prmt(r.w, 0u, (4u << 12) | ((uint32_t)k << 8) | (4u << 4) | (uint32_t)k);
-            h[k] = hfma2_u32(and_xor(x, 0x00F0000Fu, 0x64806408u), 0x2C003C00u, 0xD480E408u);
-        }
-    } else if constexpr (KIND == K_E4M3) {
-        h[0] = e4m3x2_to_half2(r.w.x & 0xffffu);
-        h[1] = e4m3x2_to_half2(r.w.x >> 16);
-        h[2] = e4m3x2_to_half2(r.w.y & 0xffffu);
-        h[3] = e4m3x2_to_half2(r.w.y >> 16);
-    } else {
-        h[0] = r.w.x; h[1] = r.w.y; h[2] = r.w.z; h[3] = r.w.w;
-    }
-}
-
 // Scales of one token as the converters see them.
 struct RowScale {
     int e;        // exponent of the largest group scale (grouped)
@@ -1198,27 +1139,12 @@ cudaError_t launch(const TreeParams &p, cudaStream_t stream)
             if (dev < 64) ready[dev] = true;
         }
     }
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(p.l.num_ctas);
-    lc.blockDim = dim3(kThreads);
-    lc.dynamicSmemBytes = p.l.smem_bytes;
-    lc.stream = stream;
-    lc.attrs = attr;
-    lc.numAttrs = 1;
-    void *args[] = {const_cast<TreeParams *>(&p)};
-    (void)cudaGetLastError();
-    e = cudaLaunchKernelExC(&lc, fn, args);
+    e = launch_dependent(tree_kernel<DH>, (unsigned)p.l.num_ctas, kThreads, p.l.smem_bytes, stream, p);
     if (e != cudaSuccess) return e;
     const int64_t rows = (int64_t)p.rows.batch * p.rows.heads * p.n_tree * p.G;
     const int64_t blocks = (rows + 7) / 8;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    lc.gridDim = dim3((unsigned)blocks);
-    lc.blockDim = dim3(256);
-    lc.dynamicSmemBytes = 0;
-    return cudaLaunchKernelExC(&lc, reinterpret_cast<void *>(&tree_merge_kernel<DH>), args);
+    return launch_dependent(tree_merge_kernel<DH>, (unsigned)blocks, 256, 0, stream, p);
 }
 
 }  // namespace
