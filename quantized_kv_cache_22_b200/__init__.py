@@ -166,11 +166,29 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+class _Memo:
+    """A place for the C struct of a Python object, emptied when one of its attributes is set."""
+    __slots__ = ("_memo", "__dict__")
+
+    def __new__(cls, *args, **kw):
+        self = object.__new__(cls)
+        object.__setattr__(self, "_memo", None)
+        return self
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if name != "_memo":
+            object.__setattr__(self, "_memo", None)
+
+    def __getstate__(self):
+        return self.__dict__.copy()     # copies and pickles make their own struct
+
+
 _CFG_MEMO = {}   # field tuple -> (KvqConfig, byref); the library only reads the struct
 
 
 @dataclass
-class Config:
+class Config(_Memo):
     """Python view of ``kvq_config`` (see include/kvq.h for the meaning of each field)."""
     batch: int
     capacity: int
@@ -206,6 +224,8 @@ class Config:
 
     def _ref(self):
         """byref() of a shared struct with these fields (read-only use by the wrappers)."""
+        if self._memo is not None:
+            return self._memo
         key = self._key()
         r = _CFG_MEMO.get(key)
         if r is None:
@@ -213,6 +233,7 @@ class Config:
                 _CFG_MEMO.clear()
             c = KvqConfig(*key)
             r = _CFG_MEMO[key] = (c, ctypes.byref(c))
+        self._memo = r[1]
         return r[1]
 
 
@@ -256,7 +277,7 @@ def kvq_h_scratch_bytes(cfg: Config, max_len: int) -> int:
 
 # ----------------------------------------------------------------------------- device buffers
 
-class LayerCache:
+class LayerCache(_Memo):
     """One layer's cache buffers, allocated with torch on `device` (caller-owned memory).
     A paged config allocates the page pool; `block_table` (int32 [B][capacity/128] on
     the device) then maps each sequence's logical pages to pool pages."""
@@ -296,13 +317,16 @@ class LayerCache:
 
     def _ref(self):
         """byref() of a struct kept for these buffers (read-only use by the wrappers)."""
-        ts = (self.k_codes, self.k_scales, self.v_codes, self.v_scales, self.block_table)
-        memo = self.__dict__.get("_c_memo")
-        if memo is None or any(a is not b for a, b in zip(memo[0], ts)):
+        if self._memo is None:
             c = self.c()
-            memo = (ts, c, ctypes.byref(c))
-            self.__dict__["_c_memo"] = memo
-        return memo[2]
+            self._memo = (ctypes.byref(c), bytes(c))
+        return self._memo[0]
+
+    def _bytes(self) -> bytes:
+        """The struct of these buffers as bytes (for arrays of layers)."""
+        if self._memo is None:
+            self._ref()
+        return self._memo[1]
 
 
 class Workspace:
@@ -481,7 +505,7 @@ def kvq_workspace_status(ws, stream=None) -> int:
 # ----------------------------------------------------------------------------- drafted tokens
 
 @dataclass
-class RopeConfig:
+class RopeConfig(_Memo):
     """Python view of ``kvq_rope_config`` (see include/kvq.h for the meaning of each field).
     ``low`` and ``high`` default to 1 and 32 turns (YARN) or 1 and 4 (BANDS)."""
     rot_dim: int
@@ -498,6 +522,11 @@ class RopeConfig:
         high = self.high or (32.0 if self.scaling == KVQ_ROPE_YARN else 4.0)
         return KvqRopeConfig(self.rot_dim, self.layout, self.scaling, self.orig_len, self.base,
                              self.factor, self.low, high, self.gain)
+
+    def _ref(self):
+        if self._memo is None:
+            self._memo = ctypes.byref(self.c())
+        return self._memo
 
 
 class TreeWorkspace(Workspace):
@@ -517,32 +546,40 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _here(*tensors):
-    """The kernels run on the current device: every tensor has to be there."""
-    dev = torch.cuda.current_device()
+def _here(stream, *tensors):
+    """The kernels run on the current device: every tensor has to be there.  Returns the stream's
+    handle (the current one's for None)."""
+    dev = torch._C._cuda_getDevice()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _ints(t, shape, what: str):
-    if t is not None and (t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous()):
+    if t is not None and (t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous()):
         raise ValueError(f"{what} is a contiguous int32 tensor of shape {tuple(shape)}")
 
 
 def _rows(t: torch.Tensor, n: int, heads: int, dim: int, batch: int, dtype, what: str):
-    """byref() of the kvq_rows of a [B][n][heads][dim] view (or None)."""
+    """The kvq_rows of a [B][n][heads][dim] view (None for None)."""
     if t is None:
         return None
-    if t.shape != (batch, n, heads, dim) or t.dtype != dtype:
+    if t.shape != (batch, n, heads, dim) or t.dtype is not dtype:
         raise ValueError(f"{what} is {dtype} of shape {(batch, n, heads, dim)}")
     sb, st, sh, sd = t.stride()
-    if t.numel() and ((sd != 1 and dim > 1) or (sh != dim and heads > 1)):
+    if (sd != 1 and dim > 1 or sh != dim and heads > 1) and t.numel():
         raise ValueError(f"the heads of a token of {what} are contiguous")
-    if (sb == 0 and batch > 1) or (st == 0 and n > 1):
-        raise ValueError(f"{what} is an expanded view: its rows share memory")
     # a stride that no index uses is whatever torch says: 0 selects the contiguous one
-    return ctypes.byref(KvqRows(t.data_ptr(), sb if batch > 1 else 0, st if n > 1 else 0))
+    if batch == 1:
+        sb = 0
+    elif sb == 0:
+        raise ValueError(f"{what} is an expanded view: its rows share memory")
+    if n == 1:
+        st = 0
+    elif st == 0 and n:
+        raise ValueError(f"{what} is an expanded view: its rows share memory")
+    return KvqRows(t.data_ptr(), sb, st)
 
 
 def kvq_rope_table(rope: RopeConfig, n_pos: int, first_pos: int = 0, table=None, device="cuda",
@@ -552,9 +589,8 @@ def kvq_rope_table(rope: RopeConfig, n_pos: int, first_pos: int = 0, table=None,
         table = torch.empty(n_pos, rope.rot_dim // 2, 2, dtype=torch.float32, device=device)
     _need(table.dtype == torch.float32 and table.is_contiguous() and
           table.shape == (n_pos, rope.rot_dim // 2, 2), "table is contiguous float32 [n_pos][rot_dim/2][2]")
-    _here(table)
-    _check("kvq_rope_table", _lib.kvq_rope_table(ctypes.byref(rope.c()), int(first_pos), int(n_pos),
-                                                 _ptr(table), _stream(stream)))
+    _check("kvq_rope_table", _lib.kvq_rope_table(rope._ref(), int(first_pos), int(n_pos),
+                                                 _ptr(table), _here(stream, table)))
     return table
 
 
@@ -567,17 +603,17 @@ def kvq_rope_append(cfg: Config, layer: LayerCache, rope: RopeConfig, table: tor
     B, n = k.shape[:2]
     _need(table.dtype == torch.float32 and table.is_contiguous() and table.dim() == 3 and
           table.shape[1:] == (rope.rot_dim // 2, 2), "table is contiguous float32 [positions][rot_dim/2][2]")
-    _here(layer.k_codes, table, q, k, v, q_out, d_pos, d_count, d_rope_pos)
+    st = _here(stream, layer.k_codes, table, q, k, v, q_out, d_pos, d_count, d_rope_pos)
     _ints(d_pos, (cfg.batch,), "d_pos")
     _ints(d_count, (cfg.batch,), "d_count")
     _ints(d_rope_pos, (cfg.batch, n), "d_rope_pos")
     _check("kvq_rope_append", _lib.kvq_rope_append(
-        cfg._ref(), layer._ref(), ctypes.byref(rope.c()), _ptr(table), table.shape[0],
+        cfg._ref(), layer._ref(), rope._ref(), _ptr(table), table.shape[0],
         _rows(q, n, cfg.n_q_heads, cfg.head_dim, cfg.batch, k.dtype, "q"),
         _rows(k, n, cfg.n_kv_heads, cfg.head_dim, cfg.batch, k.dtype, "k"),
         _rows(v, n, cfg.n_kv_heads, cfg.head_dim, cfg.batch, k.dtype, "v"),
         _rows(q_out, n, cfg.n_q_heads, cfg.head_dim, cfg.batch, k.dtype, "q_out"),
-        _dtype_code(k), _ptr(d_pos), int(max_pos), n, _ptr(d_count), _ptr(d_rope_pos), _stream(stream)))
+        _dtype_code(k), _ptr(d_pos), int(max_pos), n, _ptr(d_count), _ptr(d_rope_pos), st))
 
 
 def kvq_read(cfg: Config, layer: LayerCache, k_out, v_out, d_pos: torch.Tensor, max_pos: int, d_count=None,
@@ -587,7 +623,7 @@ def kvq_read(cfg: Config, layer: LayerCache, k_out, v_out, d_pos: torch.Tensor, 
     some = k_out if k_out is not None else v_out
     _need(some is not None, "k_out or v_out is given")
     n = some.shape[1]
-    _here(layer.k_codes, k_out, v_out, d_pos, d_count)
+    st = _here(stream, layer.k_codes, k_out, v_out, d_pos, d_count)
     _ints(d_pos, (cfg.batch,), "d_pos")
     _ints(d_count, (cfg.batch,), "d_count")
     heads, dim = cfg.n_kv_heads, cfg.head_dim
@@ -597,7 +633,7 @@ def kvq_read(cfg: Config, layer: LayerCache, k_out, v_out, d_pos: torch.Tensor, 
     _check("kvq_read", _lib.kvq_read(
         cfg._ref(), layer._ref(), _rows(k_out, n, heads, dim, cfg.batch, some.dtype, "k_out"),
         _rows(v_out, n, heads, dim, cfg.batch, some.dtype, "v_out"), _dtype_code(some), _ptr(d_pos),
-        int(max_pos), n, _ptr(d_count), _stream(stream)))
+        int(max_pos), n, _ptr(d_count), st))
 
 
 def kvq_tree_attn(cfg: Config, layer: LayerCache, q: torch.Tensor, d_len: torch.Tensor, max_len: int, d_mask,
@@ -611,13 +647,12 @@ def kvq_tree_attn(cfg: Config, layer: LayerCache, q: torch.Tensor, d_len: torch.
     if d_mask is not None:
         _need(d_mask.dtype == torch.int64 and d_mask.shape == shape[:2] and d_mask.is_contiguous(),
               "d_mask is a contiguous int64 tensor [B][n_tree]")
-    _here(layer.k_codes, q, d_len, d_mask, d_n_tree, out, ws.buf)
+    st = _here(stream, layer.k_codes, q, d_len, d_mask, d_n_tree, out, ws.buf)
     _ints(d_len, (cfg.batch,), "d_len")
     _ints(d_n_tree, (cfg.batch,), "d_n_tree")
     _check("kvq_tree_attn", _lib.kvq_tree_attn(
         cfg._ref(), layer._ref(), _ptr(q), _dtype_code(q), shape[1], _ptr(d_len), int(max_len), _ptr(d_n_tree),
-        _ptr(d_mask), float(softmax_scale), _ptr(out), _dtype_code(out), _ptr(ws.buf), ws.nbytes, int(num_ctas),
-        _stream(stream)))
+        _ptr(d_mask), float(softmax_scale), _ptr(out), _dtype_code(out), _ptr(ws.buf), ws.nbytes, int(num_ctas), st))
 
 
 def kvq_tree_commit(cfg: Config, layers, d_len: torch.Tensor, max_len: int, d_path: torch.Tensor,
@@ -625,12 +660,12 @@ def kvq_tree_commit(cfg: Config, layers, d_len: torch.Tensor, max_len: int, d_pa
     """Keep the accepted path of every sequence in all `layers` (LayerCache objects) at once:
     row d_len + path[i] moves to d_len + i; d_len_out receives d_len + the path's length."""
     _need(d_path.dim() == 2, "d_path is a contiguous int32 tensor [B][n]")
-    _here(d_len, d_path, d_n_path, d_len_out, *(x.k_codes for x in layers))
+    st = _here(stream, d_len, d_path, d_n_path, d_len_out, *[x.k_codes for x in layers])
     _ints(d_len, (cfg.batch,), "d_len")
     _ints(d_path, (cfg.batch, d_path.shape[1]), "d_path")
     _ints(d_n_path, (cfg.batch,), "d_n_path")
     _ints(d_len_out, (cfg.batch,), "d_len_out")
-    arr = (KvqLayer * len(layers))(*(x.c() for x in layers))
+    arr = (KvqLayer * len(layers)).from_buffer_copy(b"".join([x._bytes() for x in layers]))
     _check("kvq_tree_commit", _lib.kvq_tree_commit(
         cfg._ref(), arr, len(layers), _ptr(d_len), int(max_len), int(n_tree), _ptr(d_path), d_path.shape[1],
-        _ptr(d_n_path), _ptr(d_len_out), _stream(stream)))
+        _ptr(d_n_path), _ptr(d_len_out), st))
