@@ -81,7 +81,7 @@ struct Ctl {
     uint32_t tmem;
     int abort;
     float m[TT];                        // what O is scaled by, per TMEM lane
-    float2 ml[2][TT];                   // (m, l) of the groups
+    alignas(16) float2 ml[TT][2];       // (m, l) of the groups
 };
 // Per-token numbers of a tile, four tiles deep: the converters run at most two tiles ahead of
 // the softmax.
@@ -92,8 +92,7 @@ template <int N>
 struct Int {
     static constexpr int value = N;
 };
-constexpr int STAGE_LD = 17;            // floats per row of the epilogue's 16-column staging
-constexpr int STAGE_BYTES = 2 * TT * STAGE_LD * 4;
+constexpr int STAGE_BYTES = 2 * TT * 64;    // the epilogue's staging: 16 columns of a row by each group
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -620,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         const uint32_t lane_off = (uint32_t)(place & ~31) << 16;
         const uint32_t s_row = tmem + COL_S + 128u * grp + lane_off, o_row = tmem + COL_O + lane_off;
         const uint32_t p_row = over ? s_row : tmem + COL_P + lane_off;
-        float *stage = reinterpret_cast<float *>(smem + keep(p.l.off_stage));
+        float4 *stage = reinterpret_cast<float4 *>(smem + keep(p.l.off_stage));
         const float osign = p.fmt == KVQ_FMT_TENSOR && __half2float(p.v.scales[0]) < 0.f ? -1.f : 1.f;
         // A wait that gave up does not end the role: the eight warps meet at a hardware barrier
         // at every segment's end, so all of them walk on to the end (with the abort flag up no
@@ -644,7 +643,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             uint64_t mask;                           // drafted tokens that the row attends
         };
         // this thread's row of the walk's segment; store: its query into TMEM
-        auto open = [&](const Walk &o, bool store) {
+        // (once free_q() says that the scores of the segment before are done)
+        auto open = [&](const Walk &o, bool store, auto &&free_q) {
             Row x;
             x.rows = min(kTreeRows, o.s.n * p.G - o.rt * kTreeRows);
             x.copies = x.rows <= 32 ? 4 : x.rows <= 64 ? 2 : 1;
@@ -669,30 +669,41 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 return pow2i(-ex);
             };
             if (p.q_dtype == KVQ_F16 && !store) return x;
+            // (loops kept rolled: this runs once a segment, and code that is not in the
+            // instruction cache takes longer to fetch than to run)
             if (p.q_dtype != KVQ_F32) {
-                // the whole row at once, one wait for memory
-                uint4 u[DH / 8];
                 const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + at);
-#pragma unroll
-                for (int k = 0; k < DH / 8; k++) u[k] = live ? src[k] : make_uint4(0u, 0u, 0u, 0u);
-                uint32_t *h = reinterpret_cast<uint32_t *>(u);
+                const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+                float pre = 1.f;
                 if (p.q_dtype == KVQ_BF16) {
-                    // (bf16 magnitudes compare as integers, the high one of a pair above its low one)
-                    uint32_t top = 0u, low = 0u;
+                    uint32_t top = 0u;                              // (bf16 magnitudes compare as integers)
+#pragma unroll 1
+                    for (int c = 0; c < DH / 8; c += 8) {
+                        uint4 u[8];
 #pragma unroll
-                    for (int k = 0; k < DH / 2; k++) {
-                        top = max(top, h[k] & 0x7fff0000u);
-                        low = max(low, h[k] & 0x00007fffu);
+                        for (int k = 0; k < 8; k++) u[k] = live ? src[c + k] : none;
+#pragma unroll
+                        for (int k = 0; k < 8; k++) {
+                            top = __vmaxu2(top, __vmaxu2(u[k].x & 0x7fff7fffu, u[k].y & 0x7fff7fffu));
+                            top = __vmaxu2(top, __vmaxu2(u[k].z & 0x7fff7fffu, u[k].w & 0x7fff7fffu));
+                        }
                     }
-                    const float pre = level(__uint_as_float(max(top, low << 16)));
+                    pre = level(__uint_as_float(max(top & 0xffff0000u, top << 16)));
                     if (!store) return x;
-#pragma unroll
-                    for (int k = 0; k < DH / 2; k++)
-                        h[k] = pack_half2(__uint_as_float(h[k] << 16) * pre, __uint_as_float(h[k] & 0xffff0000u) * pre);
                 }
+                free_q();
+#pragma unroll 1
+                for (int c = 0; c < DH / 32; c++) {
+                    uint4 u[4];
 #pragma unroll
-                for (int k = 0; k < DH / 32; k++)
-                    tmem_st16(tmem + COL_Q + lane_off + 16u * k, *reinterpret_cast<uint32_t(*)[16]>(h + 16 * k));
+                    for (int k = 0; k < 4; k++) u[k] = live ? src[4 * c + k] : none;
+                    uint32_t *h = reinterpret_cast<uint32_t *>(u);
+                    if (p.q_dtype == KVQ_BF16)
+#pragma unroll
+                        for (int k = 0; k < 16; k++)
+                            h[k] = pack_half2(__uint_as_float(h[k] << 16) * pre, __uint_as_float(h[k] & 0xffff0000u) * pre);
+                    tmem_st16(tmem + COL_Q + lane_off + 16u * c, *reinterpret_cast<uint32_t(*)[16]>(h));
+                }
             } else {
                 const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(p.q) + at);
                 const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -704,6 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 }
                 const float pre = level(a);
                 if (!store) return x;
+                free_q();
 #pragma unroll 1
                 for (int c = 0; c < DH / 32; c++) {
                     uint32_t hi[16], lo[16];
@@ -862,11 +874,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             Row next{};
             if (ahead.count) {
                 const bool mine = (i & 1) == grp;
-                if (mine && opened) {
+                next = open(ahead, mine, [&]() {
+                    if (!opened) return;
                     hold(&ctl->sfull[last & 1], last >> 1);
                     tc_fence_after();
-                }
-                next = open(ahead, mine);
+                });
                 tc_fence_before();
                 __syncwarp();
                 if (mine || ahead.count > 1) mbar_arrive_if(&ctl->sready[grp], lane == 0);
@@ -878,56 +890,96 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             }
             // ---- join the groups' sums and the copies of every row; the output, or a partial
             const int nr = TT / copies, r = place & (nr - 1), rows = row.rows;
-            ctl->ml[grp][place] = make_float2(m, l);
+            const bool direct = it.tile == 0 && it.count == it.s.tiles;
+            // a CTA leaves two partials at most: of its first segment, and of its last
+            float *part = p.slots + (int64_t)(2 * (int)blockIdx.x + (i0 == 0 ? 0 : 1)) * tree_slot_floats(p.slot_rows, DH);
+            float *part_ml = part + (int64_t)p.slot_rows * DH + 2 * place;
+            int64_t out0 = ((int64_t)it.b * p.n_tree * p.n_q_heads + (int64_t)it.head * p.G) * DH;
+            float per_g = 1.f / (float)p.G;
+            int out_dtype = p.out_dtype, q_gap = p.n_q_heads - p.G;
+            // (all of it before the wait)
+            asm volatile("" : "+l"(part), "+l"(part_ml), "+l"(out0), "+f"(per_g), "+r"(out_dtype), "+r"(q_gap));
+            // where row rr of the tile goes
+            auto row_at = [&](int rr) {
+                const int gr = it.rt * kTreeRows + rr;
+                return out0 + ((int64_t)(int)(((float)gr + 0.5f) * per_g) * q_gap + gr) * DH;
+            };
+            ctl->ml[place][grp] = make_float2(m, l);
             hold(&ctl->pvdone[last & 1], last >> 1);
             tc_fence_after();
             soft_sync();
+            float4 x[4];                                             // m, l of a copy from either group
             float M = -INFINITY, L = 0.f;
-#pragma unroll 1
-            for (int c = r; c < TT; c += nr) M = fmaxf(M, ctl->m[c]);
-#pragma unroll 1
-            for (int c = r; c < 2 * TT; c += nr) {
-                const float2 x = ctl->ml[0][c];
-                L += x.x == -INFINITY ? 0.f : x.y * ex2(x.x - M);
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+                x[c] = c < copies ? *reinterpret_cast<const float4 *>(ctl->ml[r + c * nr])
+                                  : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+                M = fmaxf(M, fmaxf(x[c].x, x[c].z));
             }
-            const float mine = ctl->m[place];
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+                L += x[c].x == -INFINITY ? 0.f : x[c].y * ex2(x[c].x - M);
+                L += x[c].z == -INFINITY ? 0.f : x[c].w * ex2(x[c].z - M);
+            }
+            const float mine = fmaxf(ctl->ml[place][0].x, ctl->ml[place][1].x);     // what O is scaled by
+            if (grp == 0) ctl->m[place] = -INFINITY;                 // for the next segment
             float f = mine == -INFINITY ? 0.f : ex2(mine - M) * osign;
-            const long long u0 = w.u0 + i0 - it.tile, u1 = u0 + it.s.tiles;
-            const bool opens = u0 >= w.u0, direct = opens && u1 <= w.u0 + n_units;
-            // a CTA leaves two partials at most: of its first segment, and of its last
-            const int slot = 2 * (int)blockIdx.x + (i0 == 0 ? 0 : 1);
-            float *part = p.slots + (int64_t)slot * tree_slot_floats(p.slot_rows, DH);
             if (direct) f = L != 0.f ? f / L : 0.f;
-            if (threadIdx.x == 0 && opens && ok)
-                p.seg[((int64_t)it.b * p.rows.heads + it.head) * p.row_tiles + it.rt] =
-                    make_int4(slot, blockIdx.x, direct ? 1 : range_cta(u1 - 1, w.n, w.p) - (int)blockIdx.x + 1, 0);
-            if (!direct && ok && threadIdx.x < rows)
-                *reinterpret_cast<float2 *>(part + (int64_t)p.slot_rows * DH + 2 * place) = make_float2(M, L);
-            // 32 columns of O a round, 16 by each group; then eight lanes a row, four columns each
-            const int r0 = threadIdx.x >> 3, half = (threadIdx.x >> 2) & 1, col = (threadIdx.x & 3) * 4;
-            const int64_t out0 = ((int64_t)it.b * p.n_tree * p.n_q_heads + (int64_t)it.head * p.G) * DH;
+            if (!direct && ok && threadIdx.x < rows) *reinterpret_cast<float2 *>(part_ml) = make_float2(M, L);
+            if (copies == 1) {
+                // every thread has a row's sums: half of its columns, 16 a time
+                const int64_t at = (direct ? row_at(place) : (int64_t)place * DH) + DH / 2 * grp;
 #pragma unroll 1
-            for (int c = 0; c < DH; c += 32) {
-                uint32_t o[16];
-                tmem_ld16(o_row + c + 16u * grp, o);
-                if (c > 0) soft_sync();                              // the staging was read
+                for (int c = 0; c < DH / 2; c += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(o_row + c + DH / 2 * grp, o);
+                    float y[16];
 #pragma unroll
-                for (int x = 0; x < 16; x++)
-                    stage[(grp * TT + place) * STAGE_LD + x] = f == 0.f ? 0.f : __uint_as_float(o[x]) * f;
+                    for (int k = 0; k < 16; k++) y[k] = f == 0.f ? 0.f : __uint_as_float(o[k]) * f;
+                    if (place < rows && ok) {
+                        if (direct) {
+                            store8(p.out, at + c, out_dtype, *reinterpret_cast<float(*)[8]>(y));
+                            store8(p.out, at + c + 8, out_dtype, *reinterpret_cast<float(*)[8]>(y + 8));
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; k++) reinterpret_cast<float4 *>(part + at + c)[k] = reinterpret_cast<float4 *>(y)[k];
+                        }
+                    }
+                }
                 soft_sync();
-                if (c == 0 && grp == 0) ctl->m[place] = -INFINITY;   // for the next segment
+            } else {
+                // 32 columns of O a round, 16 by each group; then eight lanes a row, four columns
+                // each.  Staged rows are 64 bytes, their 16-byte pieces permuted so that neither
+                // side meets bank conflicts.
+                const int r0 = threadIdx.x >> 3, half = (threadIdx.x >> 2) & 1, piece = threadIdx.x & 3;
+                float4 *put = stage + (grp * TT + (place ^ grp)) * 4;
+                const int put_x = (place >> 1) & 3;
 #pragma unroll 1
-                for (int rr = r0; rr < rows && ok; rr += 32) {
-                    float y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-                    for (int q = rr; q < TT; q += nr)
+                for (int c = 0; c < DH; c += 32) {
+                    uint32_t o[16];
+                    tmem_ld16(o_row + c + 16u * grp, o);
 #pragma unroll
-                        for (int d = 0; d < 4; d++) y[d] += stage[(half * TT + q) * STAGE_LD + col + d];
-                    const int gr = it.rt * kTreeRows + rr, qi = gr / p.G, at = c + 16 * half + col;
-                    if (direct)
-                        store4(p.out, out0 + ((int64_t)qi * (p.n_q_heads - p.G) + gr) * DH + at, p.out_dtype, y);
-                    else
-                        *reinterpret_cast<float4 *>(part + rr * DH + at) = make_float4(y[0], y[1], y[2], y[3]);
+                    for (int k = 0; k < 16; k++) o[k] = f == 0.f ? 0u : __float_as_uint(__uint_as_float(o[k]) * f);
+                    if (c > 0) soft_sync();                          // the staging was read
+#pragma unroll
+                    for (int k = 0; k < 4; k++) put[k ^ put_x] = reinterpret_cast<float4 *>(o)[k];
+                    soft_sync();
+#pragma unroll 1
+                    for (int rr = r0; rr < rows && ok; rr += 32) {
+                        float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            if (k >= copies) break;
+                            const int q = rr + k * nr;
+                            const float4 v = stage[(half * TT + (q ^ half)) * 4 + (piece ^ ((q >> 1) & 3))];
+                            y[0] += v.x, y[1] += v.y, y[2] += v.z, y[3] += v.w;
+                        }
+                        const int at = c + 16 * half + 4 * piece;
+                        if (direct)
+                            store4(p.out, row_at(rr) + at, out_dtype, y);
+                        else
+                            *reinterpret_cast<float4 *>(part + rr * DH + at) = make_float4(y[0], y[1], y[2], y[3]);
+                    }
                 }
             }
             m = -INFINITY;
@@ -1064,6 +1116,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 (void)mbar_wait_drain(&ctl->drain, 0, limit);
             }
             __syncwarp();
+        } else if (warp == kMmaWarp + 1 && lane == 0) {
+            // ====================== where the partials are ======================
+            // of every row tile whose first tokens are this CTA's: the slot of its first partial,
+            // the CTA, how many CTAs share it
+            Walk it;
+            int done = 0;
+#pragma unroll 1
+            for (it.start(p, w); it.count; it.next(p)) {
+                if (it.tile == 0)
+                    p.seg[((int64_t)it.b * p.rows.heads + it.head) * p.row_tiles + it.rt] =
+                        make_int4(2 * (int)blockIdx.x + (done == 0 ? 0 : 1), blockIdx.x,
+                                  it.count == it.s.tiles ? 1 : range_cta(w.u0 + done + it.s.tiles - 1, w.n, w.p) - (int)blockIdx.x + 1, 0);
+                done += it.count;
+            }
         }
     }
 
@@ -1080,11 +1146,9 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__
     grid_dependency_wait();
     grid_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int R = p.n_tree * p.G;
-    if (i >= (int64_t)p.rows.batch * p.rows.heads * R) return;
-    const int rr = (int)(i % R);
-    const int head = (int)(i / R % p.rows.heads), b = (int)(i / R / p.rows.heads);
+    const unsigned blocks = (unsigned)(p.n_tree * p.G + 7) / 8, at_bh = blockIdx.x / blocks;
+    const int rr = (int)(blockIdx.x - at_bh * blocks) * 8 + (int)(threadIdx.x >> 5);
+    const int b = (int)(at_bh / (unsigned)p.rows.heads), head = (int)(at_bh - (unsigned)b * (unsigned)p.rows.heads);
     const Seq s = sequence(p, b);
     if (rr >= s.n * p.G) return;
     const int4 seg = p.seg[((int64_t)b * p.rows.heads + head) * p.row_tiles + rr / kTreeRows];
@@ -1141,8 +1205,7 @@ cudaError_t launch(const TreeParams &p, cudaStream_t stream)
     }
     e = launch_dependent(tree_kernel<DH>, (unsigned)p.l.num_ctas, kThreads, p.l.smem_bytes, stream, p);
     if (e != cudaSuccess) return e;
-    const int64_t rows = (int64_t)p.rows.batch * p.rows.heads * p.n_tree * p.G;
-    const int64_t blocks = (rows + 7) / 8;
+    const int64_t blocks = (int64_t)p.rows.batch * p.rows.heads * ((p.n_tree * p.G + 7) / 8);
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     return launch_dependent(tree_merge_kernel<DH>, (unsigned)blocks, 256, 0, stream, p);
 }
