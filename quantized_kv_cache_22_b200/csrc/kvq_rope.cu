@@ -55,7 +55,7 @@ __device__ __forceinline__ void codes_of(const float (&x)[8], float s, float inv
 // Quantise a row that LPR lanes hold, lane t elements 8t .. 8t+7 (v[0]) and DH/2 + 8t .. (v[1]),
 // as quantize4 does: the same codes and scales bit for bit.
 template <int DH>
-__device__ __forceinline__ void quantize_row16(const float (&v)[2][8], bool active, int t, int bits, int group, int fmt,
+__device__ __forceinline__ void quantize_row16(const float (&v)[2][8], bool active, int t, int bits, int gshift, int fmt,
                                                uint8_t *codes, __half *scales)
 {
     constexpr int LPR = DH / 16;
@@ -69,8 +69,8 @@ __device__ __forceinline__ void quantize_row16(const float (&v)[2][8], bool acti
         return;
     }
     // lanes of a group's half, and whether both halves are one group
-    const bool joint = group == DH;
-    const int span = min(group >> 3, LPR);
+    const bool joint = (1 << gshift) == DH;
+    const int span = min(1 << (gshift - 3), LPR);
     float lo[2], hi[2];                          // per half: least and largest, or largest magnitude
 #pragma unroll
     for (int h = 0; h < 2; h++) {
@@ -157,38 +157,53 @@ __device__ __forceinline__ void quantize_row16(const float (&v)[2][8], bool acti
         } else {
             *reinterpret_cast<uint2 *>(codes + e0) = make_uint2(w[0], w[1]);
         }
-        if (fmt != KVQ_FMT_TENSOR && t % span == 0 && !(h == 1 && joint)) {
+        if (fmt != KVQ_FMT_TENSOR && (t & (span - 1)) == 0 && !(h == 1 && joint)) {
             if (fmt == KVQ_FMT_ASYM)
-                reinterpret_cast<__half2 *>(scales)[e0 / group] = __halves2half2(s16, __int2half_rn(z));
+                reinterpret_cast<__half2 *>(scales)[e0 >> gshift] = __halves2half2(s16, __int2half_rn(z));
             else
-                scales[e0 / group] = s16;
+                scales[e0 >> gshift] = s16;
         }
     }
 }
 
-__device__ __forceinline__ void load8(const void *base, int64_t idx, int dtype, float (&x)[8])
-{
-    if (dtype == KVQ_F32) {
-        const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + idx);
-        const float4 a = src[0], b = src[1];
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-        return;
-    }
-    const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + idx);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// A lane's 16 elements as they lie in memory: eight of each half of the row.
+template <int DT>
+struct Raw16 {
+    static constexpr int N = DT == KVQ_F32 ? 2 : 1;
+    uint4 u[2][N];
+    template <int DH>
+    __device__ __forceinline__ void load(const void *base, int64_t idx)
+    {
+        constexpr int B = DT == KVQ_F32 ? 4 : 2;
+        const uint8_t *src = static_cast<const uint8_t *>(base) + idx * B;
 #pragma unroll
-    for (int k = 0; k < 4; k++) {
-        if (dtype == KVQ_F16) {
-            const float2 f = unpack_half2(w[k]);
-            x[2 * k] = f.x;
-            x[2 * k + 1] = f.y;
-        } else {
-            x[2 * k] = __uint_as_float(w[k] << 16);
-            x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-        }
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+            for (int k = 0; k < N; k++) u[h][k] = *reinterpret_cast<const uint4 *>(src + h * (DH / 2) * B + 16 * k);
     }
-}
+    __device__ __forceinline__ void values(float (&x)[2][8]) const
+    {
+#pragma unroll
+        for (int h = 0; h < 2; h++)
+#pragma unroll
+            for (int k = 0; k < N; k++) {
+                const uint32_t w[4] = {u[h][k].x, u[h][k].y, u[h][k].z, u[h][k].w};
+#pragma unroll
+                for (int q = 0; q < 4; q++) {
+                    if constexpr (DT == KVQ_F32) {
+                        x[h][4 * k + q] = __uint_as_float(w[q]);
+                    } else if constexpr (DT == KVQ_F16) {
+                        const float2 f = unpack_half2(w[q]);
+                        x[h][2 * q] = f.x;
+                        x[h][2 * q + 1] = f.y;
+                    } else {
+                        x[h][2 * q] = __uint_as_float(w[q] << 16);
+                        x[h][2 * q + 1] = __uint_as_float(w[q] & 0xffff0000u);
+                    }
+                }
+            }
+    }
+};
 
 // A row is DH/16 lanes of 16 elements, eight in each half of the row, so that a warp's loads
 // and stores are whole 16-byte runs and the pairs of a fully rotated half layout meet in one
@@ -238,7 +253,8 @@ struct Turn {
     // The lane's elements x of the row whose element 0 is src[at], turned.  Every product and
     // sum is rounded on its own (no fused multiply-add), so that codes and scales match an IEEE
     // reference bit for bit.
-    __device__ __forceinline__ void apply(float (&x)[2][8], const void *src, int64_t at, int dtype, bool valid) const
+    template <int DT>
+    __device__ __forceinline__ void apply(float (&x)[2][8], const void *src, int64_t at) const
     {
         if constexpr (MODE == 0) {
 #pragma unroll
@@ -263,9 +279,9 @@ struct Turn {
             for (int k = 0; k < 4; k++) {
                 const int h = k >> 1, e = h * DH / 2 + 8 * t + 4 * (k & 1);
                 const bool upper = e >= half;
-                if (turned[h] && valid) {
+                if (turned[h]) {
                     float o[4];
-                    load4(src, at + (upper ? e - half : e + half), dtype, o);
+                    load4(src, at + (upper ? e - half : e + half), DT, o);
 #pragma unroll
                     for (int q = 0; q < 4; q++) {
                         const float a = __fmul_rn(x[h][4 * (k & 1) + q], c[4 * k + q]), d = __fmul_rn(o[q], s[4 * k + q]);
@@ -280,8 +296,8 @@ struct Turn {
 
 constexpr unsigned kRopeWarps = 4;               // a block
 
-template <int DH, int MODE>
-__global__ void __launch_bounds__(32 * kRopeWarps, MODE == 2 ? 5 : 7)
+template <int DH, int MODE, int DT>
+__global__ void __launch_bounds__(32 * kRopeWarps, MODE == 2 ? 4 : 5)
     rope_append_kernel(const __grid_constant__ RopeAppendParams p, int split)
 {
     grid_dependency_wait();
@@ -302,42 +318,37 @@ __global__ void __launch_bounds__(32 * kRopeWarps, MODE == 2 ? 5 : 7)
     const int sub = lane / LPR, t = lane % LPR;
     Turn<DH, MODE> turn;
     turn.load(p.table + rp * (p.rot >> 1), p.rot, t);
-    // row `sub` of unit u of a tensor with `heads` rows
-    auto load_row = [&](const RowsView &r, int u, int heads, float (&x)[2][8], int64_t &at) {
-        const int head = u * RPW + sub;
-        const bool valid = head < heads;
-        at = b * r.batch_stride + j * r.token_stride + (int64_t)head * DH;
-#pragma unroll
-        for (int h = 0; h < 2; h++)
-#pragma unroll
-            for (int e = 0; e < 8; e++) x[h][e] = 0.f;
-        if (valid) {
-            load8(r.data, at + 8 * t, p.dtype, x[0]);
-            load8(r.data, at + DH / 2 + 8 * t, p.dtype, x[1]);
-        }
-        return valid;
-    };
+    // A unit is RPW heads of a tensor; behind the last head a lane works on that one again, and
+    // stores nothing.
+    auto row_of = [&](const RowsView &r) { return b * r.batch_stride + j * r.token_stride; };
     const int Hq = p.q_in.data ? p.n_q_heads : 0, Hkv = p.rows.heads;
     const int nq = (Hq + RPW - 1) / RPW, nk = (Hkv + RPW - 1) / RPW;
     int i = (int)(w - token * (unsigned)split);
+    if (i < nq) {
+        constexpr int U = DT == KVQ_F32 || MODE == 2 ? 2 : 4;            // units in flight
+        const int64_t from = row_of(p.q_in), to = row_of(p.q_out) + 8 * t;
 #pragma unroll 1
-    for (; i < nq; i += 2 * split) {
-        float x[2][2][8];
-        int64_t at[2];
-        bool valid[2];
+        for (; i < nq; i += U * split) {
+            Raw16<DT> raw[U];
 #pragma unroll
-        for (int u = 0; u < 2; u++) valid[u] = load_row(p.q_in, i + u * split, i + u * split < nq ? Hq : 0, x[u], at[u]);
+            for (int u = 0; u < U; u++)
+                if (u == 0 || i + u * split < nq)
+                    raw[u].template load<DH>(p.q_in.data, from + min((i + u * split) * RPW + sub, Hq - 1) * DH + 8 * t);
 #pragma unroll
-        for (int u = 0; u < 2; u++) {
-            turn.apply(x[u], p.q_in.data, at[u], p.dtype, valid[u]);
-            if (valid[u]) {
-                const int64_t to = b * p.q_out.batch_stride + j * p.q_out.token_stride + (int64_t)((i + u * split) * RPW + sub) * DH + 8 * t;
-                store8(p.q_out.data, to, p.dtype, x[u][0]);
-                store8(p.q_out.data, to + DH / 2, p.dtype, x[u][1]);
+            for (int u = 0; u < U; u++) {
+                const int head = (i + u * split) * RPW + sub;
+                if (u > 0 && i + u * split >= nq) break;
+                float x[2][8];
+                raw[u].values(x);
+                turn.template apply<DT>(x, p.q_in.data, from + min(head, Hq - 1) * DH);
+                if (head < Hq) {
+                    store8(p.q_out.data, to + head * DH, DT, x[0]);
+                    store8(p.q_out.data, to + head * DH + DH / 2, DT, x[1]);
+                }
             }
         }
+        while (i - split >= nq) i -= split;      // (units past the last query's were skipped)
     }
-    if (i - split >= nq) i -= split;             // (the last pair had one unit only)
     i -= nq;
     // a token that a later token of this call overwrites in the ring is not stored
     bool keep = true;
@@ -345,29 +356,48 @@ __global__ void __launch_bounds__(32 * kRopeWarps, MODE == 2 ? 5 : 7)
         keep = pos + p.rows.window > (int64_t)first + count - 1;
     const int64_t row0 = keep ? cache_row(p.rows, b, 0, pos) : -1;       // head 0's row; heads lie apart by:
     const int64_t head_rows = p.rows.block_table ? kPageTokens : p.rows.cap;
+    const int64_t from_k = row_of(p.k_in), from_v = row_of(p.v_in);
+    auto load = [&](int at, Raw16<DT> &raw) {
+        const bool is_v = at >= nk;
+        const int head = min((is_v ? at - nk : at) * RPW + sub, Hkv - 1);
+        raw.template load<DH>(is_v ? p.v_in.data : p.k_in.data, (is_v ? from_v : from_k) + head * DH + 8 * t);
+    };
+    Raw16<DT> raw, next;
+    if (i < 2 * nk) load(i, next);
 #pragma unroll 1
     for (; i < 2 * nk; i += split) {
+        raw = next;
+        if (i + split < 2 * nk) load(i + split, next);
         const bool is_v = i >= nk;
-        const int u = is_v ? i - nk : i;
+        const int head = (is_v ? i - nk : i) * RPW + sub;
         float x[2][8];
-        int64_t at;
-        const bool valid = load_row(is_v ? p.v_in : p.k_in, u, Hkv, x, at);
-        if (!is_v) turn.apply(x, p.k_in.data, at, p.dtype, valid);
-        const CacheTensor &ten = is_v ? p.v : p.k;
-        const bool active = valid && row0 >= 0;
-        const int64_t cr = active ? row0 + (u * RPW + sub) * head_rows : 0;
-        quantize_row16<DH>(x, active, t, ten.bits, ten.group, p.fmt, ten.codes + cr * (DH * ten.bits / 8),
-                           ten.bits == 16 || p.fmt == KVQ_FMT_TENSOR
-                               ? ten.scales : ten.scales + cr * (DH / ten.group) * scale_vals(p.fmt));
+        raw.values(x);
+        if (!is_v) turn.template apply<DT>(x, p.k_in.data, from_k + min(head, Hkv - 1) * DH);
+        const int bits = is_v ? p.v.bits : p.k.bits, gshift = __ffs(is_v ? p.v.group : p.k.group) - 1;
+        uint8_t *codes = is_v ? p.v.codes : p.k.codes;
+        __half *scales = is_v ? p.v.scales : p.k.scales;
+        const bool active = head < Hkv && row0 >= 0;
+        const int64_t cr = active ? row0 + head * head_rows : 0;
+        if (bits != 16 && p.fmt != KVQ_FMT_TENSOR) scales += cr * ((DH >> gshift) * scale_vals(p.fmt));
+        quantize_row16<DH>(x, active, t, bits, gshift, p.fmt, codes + cr * (DH * bits / 8), scales);
     }
+}
+
+template <int DH, int MODE>
+cudaError_t launch_append(const RopeAppendParams &p, unsigned blocks, int split, cudaStream_t stream)
+{
+    auto kernel = p.dtype == KVQ_F32   ? rope_append_kernel<DH, MODE, KVQ_F32>
+                  : p.dtype == KVQ_F16 ? rope_append_kernel<DH, MODE, KVQ_F16>
+                                       : rope_append_kernel<DH, MODE, KVQ_BF16>;
+    return launch_dependent(kernel, blocks, 32 * kRopeWarps, 0, stream, p, split);
 }
 
 template <int DH>
 cudaError_t launch_append_dh(const RopeAppendParams &p, unsigned blocks, int split, cudaStream_t stream)
 {
-    if (p.interleaved) return launch_dependent(rope_append_kernel<DH, 1>, blocks, 32 * kRopeWarps, 0, stream, p, split);
-    if (p.rot == DH) return launch_dependent(rope_append_kernel<DH, 0>, blocks, 32 * kRopeWarps, 0, stream, p, split);
-    return launch_dependent(rope_append_kernel<DH, 2>, blocks, 32 * kRopeWarps, 0, stream, p, split);
+    if (p.interleaved) return launch_append<DH, 1>(p, blocks, split, stream);
+    if (p.rot == DH) return launch_append<DH, 0>(p, blocks, split, stream);
+    return launch_append<DH, 2>(p, blocks, split, stream);
 }
 
 }  // namespace
