@@ -315,18 +315,16 @@ class LayerCache(_Memo):
                           for t in (self.k_codes, self.k_scales, self.v_codes, self.v_scales,
                                     self.block_table)))
 
-    def _ref(self):
-        """byref() of a struct kept for these buffers (read-only use by the wrappers)."""
+    def _kept(self):
+        """A struct kept for these buffers (read-only use by the wrappers): byref() of it, its
+        bytes (for arrays of layers), the buffers' device."""
         if self._memo is None:
             c = self.c()
-            self._memo = (ctypes.byref(c), bytes(c))
-        return self._memo[0]
+            self._memo = (ctypes.byref(c), bytes(c), self.k_codes.get_device())
+        return self._memo
 
-    def _bytes(self) -> bytes:
-        """The struct of these buffers as bytes (for arrays of layers)."""
-        if self._memo is None:
-            self._ref()
-        return self._memo[1]
+    def _ref(self):
+        return self._kept()[0]
 
 
 class Workspace:
@@ -546,13 +544,16 @@ def _need(ok: bool, what: str):
         raise ValueError(what)
 
 
-def _here(stream, *tensors):
-    """The kernels run on the current device: every tensor has to be there.  Returns the stream's
-    handle (the current one's for None)."""
+def _here(stream, layers, *tensors):
+    """The kernels run on the current device: every layer and tensor has to be there.  Returns the
+    stream's handle (the current one's for None)."""
     dev = torch._C._cuda_getDevice()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+    for x in layers:
+        if x._kept()[2] != dev:
+            raise ValueError(f"a layer is on {x.k_codes.device}, the current device is cuda:{dev}")
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
@@ -590,7 +591,7 @@ def kvq_rope_table(rope: RopeConfig, n_pos: int, first_pos: int = 0, table=None,
     _need(table.dtype == torch.float32 and table.is_contiguous() and
           table.shape == (n_pos, rope.rot_dim // 2, 2), "table is contiguous float32 [n_pos][rot_dim/2][2]")
     _check("kvq_rope_table", _lib.kvq_rope_table(rope._ref(), int(first_pos), int(n_pos),
-                                                 _ptr(table), _here(stream, table)))
+                                                 _ptr(table), _here(stream, (), table)))
     return table
 
 
@@ -601,14 +602,15 @@ def kvq_rope_append(cfg: Config, layer: LayerCache, rope: RopeConfig, table: tor
     q, q_out [B][n][Hq][Dh] (both None: keys only), k, v [B][n][Hkv][Dh]: views whose token and
     batch strides are free (e.g. parts of one projection's output)."""
     B, n = k.shape[:2]
-    _need(table.dtype == torch.float32 and table.is_contiguous() and table.dim() == 3 and
-          table.shape[1:] == (rope.rot_dim // 2, 2), "table is contiguous float32 [positions][rot_dim/2][2]")
-    st = _here(stream, layer.k_codes, table, q, k, v, q_out, d_pos, d_count, d_rope_pos)
+    rows = table.shape[0] if table.dim() else 0
+    _need(table.dtype is torch.float32 and table.is_contiguous() and table.shape == (rows, rope.rot_dim // 2, 2),
+          "table is contiguous float32 [positions][rot_dim/2][2]")
+    st = _here(stream, (layer,), table, q, k, v, q_out, d_pos, d_count, d_rope_pos)
     _ints(d_pos, (cfg.batch,), "d_pos")
     _ints(d_count, (cfg.batch,), "d_count")
     _ints(d_rope_pos, (cfg.batch, n), "d_rope_pos")
     _check("kvq_rope_append", _lib.kvq_rope_append(
-        cfg._ref(), layer._ref(), rope._ref(), _ptr(table), table.shape[0],
+        cfg._ref(), layer._ref(), rope._ref(), table.data_ptr(), rows,
         _rows(q, n, cfg.n_q_heads, cfg.head_dim, cfg.batch, k.dtype, "q"),
         _rows(k, n, cfg.n_kv_heads, cfg.head_dim, cfg.batch, k.dtype, "k"),
         _rows(v, n, cfg.n_kv_heads, cfg.head_dim, cfg.batch, k.dtype, "v"),
@@ -623,7 +625,7 @@ def kvq_read(cfg: Config, layer: LayerCache, k_out, v_out, d_pos: torch.Tensor, 
     some = k_out if k_out is not None else v_out
     _need(some is not None, "k_out or v_out is given")
     n = some.shape[1]
-    st = _here(stream, layer.k_codes, k_out, v_out, d_pos, d_count)
+    st = _here(stream, (layer,), k_out, v_out, d_pos, d_count)
     _ints(d_pos, (cfg.batch,), "d_pos")
     _ints(d_count, (cfg.batch,), "d_count")
     heads, dim = cfg.n_kv_heads, cfg.head_dim
@@ -647,7 +649,7 @@ def kvq_tree_attn(cfg: Config, layer: LayerCache, q: torch.Tensor, d_len: torch.
     if d_mask is not None:
         _need(d_mask.dtype == torch.int64 and d_mask.shape == shape[:2] and d_mask.is_contiguous(),
               "d_mask is a contiguous int64 tensor [B][n_tree]")
-    st = _here(stream, layer.k_codes, q, d_len, d_mask, d_n_tree, out, ws.buf)
+    st = _here(stream, (layer,), q, d_len, d_mask, d_n_tree, out, ws.buf)
     _ints(d_len, (cfg.batch,), "d_len")
     _ints(d_n_tree, (cfg.batch,), "d_n_tree")
     _check("kvq_tree_attn", _lib.kvq_tree_attn(
@@ -660,12 +662,12 @@ def kvq_tree_commit(cfg: Config, layers, d_len: torch.Tensor, max_len: int, d_pa
     """Keep the accepted path of every sequence in all `layers` (LayerCache objects) at once:
     row d_len + path[i] moves to d_len + i; d_len_out receives d_len + the path's length."""
     _need(d_path.dim() == 2, "d_path is a contiguous int32 tensor [B][n]")
-    st = _here(stream, d_len, d_path, d_n_path, d_len_out, *[x.k_codes for x in layers])
+    st = _here(stream, layers, d_len, d_path, d_n_path, d_len_out)
     _ints(d_len, (cfg.batch,), "d_len")
     _ints(d_path, (cfg.batch, d_path.shape[1]), "d_path")
     _ints(d_n_path, (cfg.batch,), "d_n_path")
     _ints(d_len_out, (cfg.batch,), "d_len_out")
-    arr = (KvqLayer * len(layers)).from_buffer_copy(b"".join([x._bytes() for x in layers]))
+    arr = (KvqLayer * len(layers)).from_buffer_copy(b"".join([x._kept()[1] for x in layers]))
     _check("kvq_tree_commit", _lib.kvq_tree_commit(
         cfg._ref(), arr, len(layers), _ptr(d_len), int(max_len), int(n_tree), _ptr(d_path), d_path.shape[1],
         _ptr(d_n_path), _ptr(d_len_out), st))
