@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -109,16 +110,17 @@ def _load():
         "kvq_selftest_noalloc_timeout": [cfgp, layp, P, i32, P, P, i32, u64, P],
         "kvq_decode_plan_info": [cfgp, i32, ctypes.POINTER(KvqDecodePlan)],
     }
-    rowp, ropep = ctypes.POINTER(KvqRows), ctypes.POINTER(KvqRopeConfig)
+    ropep = ctypes.POINTER(KvqRopeConfig)
+    # (kvq_rows and arrays of kvq_layer are passed as their bytes)
     sig.update({
         "kvq_rope_table": [ropep, i32, i32, P, P],
-        "kvq_rope_append": [cfgp, layp, ropep, P, i32, rowp, rowp, rowp, rowp, i32, P, i32, i32, P,
+        "kvq_rope_append": [cfgp, layp, ropep, P, i32, P, P, P, P, i32, P, i32, i32, P,
                             P, P],
-        "kvq_read": [cfgp, layp, rowp, rowp, i32, P, i32, i32, P, P],
+        "kvq_read": [cfgp, layp, P, P, i32, P, i32, i32, P, P],
         "kvq_tree_workspace_bytes": [cfgp, i32, i32, pu64],
         "kvq_tree_attn": [cfgp, layp, P, i32, i32, P, i32, P, P, ctypes.c_float, P, i32, P, u64,
                           i32, P],
-        "kvq_tree_commit": [cfgp, layp, i32, P, i32, i32, P, i32, P, P, P],
+        "kvq_tree_commit": [cfgp, P, i32, P, i32, i32, P, i32, P, P, P],
     })
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -562,8 +564,11 @@ def _ints(t, shape, what: str):
         raise ValueError(f"{what} is a contiguous int32 tensor of shape {tuple(shape)}")
 
 
+_pack_rows = struct.Struct("Pqq").pack
+
+
 def _rows(t: torch.Tensor, n: int, heads: int, dim: int, batch: int, dtype, what: str):
-    """The kvq_rows of a [B][n][heads][dim] view (None for None)."""
+    """The kvq_rows of a [B][n][heads][dim] view, as its bytes (None for None)."""
     if t is None:
         return None
     if t.shape != (batch, n, heads, dim) or t.dtype is not dtype:
@@ -580,7 +585,7 @@ def _rows(t: torch.Tensor, n: int, heads: int, dim: int, batch: int, dtype, what
         st = 0
     elif st == 0 and n:
         raise ValueError(f"{what} is an expanded view: its rows share memory")
-    return KvqRows(t.data_ptr(), sb, st)
+    return _pack_rows(t.data_ptr(), sb, st)
 
 
 def kvq_rope_table(rope: RopeConfig, n_pos: int, first_pos: int = 0, table=None, device="cuda",
@@ -667,7 +672,6 @@ def kvq_tree_commit(cfg: Config, layers, d_len: torch.Tensor, max_len: int, d_pa
     _ints(d_path, (cfg.batch, d_path.shape[1]), "d_path")
     _ints(d_n_path, (cfg.batch,), "d_n_path")
     _ints(d_len_out, (cfg.batch,), "d_len_out")
-    arr = (KvqLayer * len(layers)).from_buffer_copy(b"".join([x._kept()[1] for x in layers]))
     _check("kvq_tree_commit", _lib.kvq_tree_commit(
-        cfg._ref(), arr, len(layers), _ptr(d_len), int(max_len), int(n_tree), _ptr(d_path), d_path.shape[1],
+        cfg._ref(), b"".join([x._kept()[1] for x in layers]), len(layers), _ptr(d_len), int(max_len), int(n_tree), _ptr(d_path), d_path.shape[1],
         _ptr(d_n_path), _ptr(d_len_out), st))

@@ -127,9 +127,9 @@ def test_commit_refuses(want, over):
 def test_binding_refuses_what_pointers_cannot_show():
     rows = kvq._rows
     x = torch.zeros(2, 3, 4, 128, dtype=torch.float16)
-    assert rows(x, 3, 4, 128, 2, torch.float16, "x").token_stride == 512
+    assert rows(x, 3, 4, 128, 2, torch.float16, "x") == bytes(KvqRows(x.data_ptr(), 1536, 512))
     one = rows(x[:1, :1], 1, 4, 128, 1, torch.float16, "x")       # strides that no index uses
-    assert (one.batch_stride, one.token_stride) == (0, 0)
+    assert one == bytes(KvqRows(x.data_ptr(), 0, 0))
     for bad in (x.float(), x[:, :2], x.transpose(2, 3), x[..., ::2], x[:, :, ::2], x[:, :1].expand(2, 3, 4, 128)):
         with pytest.raises(ValueError):
             rows(bad, 3, 4, 128, 2, torch.float16, "x")
