@@ -311,6 +311,9 @@ int kvq_tree_commit(const kvq_config *cfg, const kvq_layer *layers, int32_t n_la
     for (int32_t i = 0; i < n_layers; i++) {
         rc = check_kv_layer(cfg, &layers[i]);
         if (rc) return rc;
+        // (moves of the same rows by two warps would race)
+        for (int32_t j = 0; j < i; j++)
+            if (layers[j].k_codes == layers[i].k_codes || layers[j].v_codes == layers[i].v_codes) return KVQ_ERR_INVALID_ARG;
     }
     CommitParams p{};
     p.rows = cache_rows(cfg, nullptr);

@@ -172,7 +172,8 @@ struct TreeParams {
 };
 constexpr int kTreeRows = 128;
 inline int tree_row_tiles(int n_tree, int G) { return (n_tree * G + kTreeRows - 1) / kTreeRows; }
-inline int tree_slot_rows(int n_tree, int G) { return n_tree * G < kTreeRows ? n_tree * G : kTreeRows; }
+// (an even number: slots start on 16 bytes)
+inline int tree_slot_rows(int n_tree, int G) { return n_tree * G < kTreeRows ? (n_tree * G + 1) & ~1 : kTreeRows; }
 __host__ __device__ constexpr int64_t tree_slot_floats(int rows, int dh) { return (int64_t)rows * (dh + 2); }
 // Fill in the launch (but num_ctas) for this device's shared memory.
 bool plan_tree(const TreeParams &p, int max_smem, TreeLaunch *l);

@@ -54,6 +54,12 @@ def test_tree_workspace_bytes():
     assert need(1) >= 256 and need(64) >= need(1)
     assert need(0) == INVALID and need(65) == INVALID and need(4, -1) == INVALID
     assert need(4, **H) == INVALID and need(4, **WINDOW) == UNSUPPORTED
+    # partial results of a CTA (two slots each) start on 16 bytes, whatever the number of rows
+    for n in (1, 3, 5, 8):
+        for group in (1, 3, 4):
+            for dh in (64, 128):
+                over = dict(n_q_heads=2 * group, n_kv_heads=2, head_dim=dh)
+                assert (need(n, 9, **over) - need(n, 8, **over)) % 32 == 0
 
 
 def rope(cfg=None, layer=LAYER, r=None, table=P(32), table_len=256, q=KvqRows(16, 0, 0), k=KvqRows(16, 0, 0),
@@ -118,6 +124,7 @@ def commit(cfg=None, layers=(LAYER,), d_len=P(64), max_len=100, n=8, path=P(80),
     (INVALID, dict(layers=())), (INVALID, dict(d_len=None)), (INVALID, dict(path=None)), (INVALID, dict(n_path=None)),
     (INVALID, dict(max_len=-1)), (INVALID, dict(n=0)), (INVALID, dict(n=65, stride=8)), (INVALID, dict(stride=0)),
     (INVALID, dict(stride=9)), (INVALID, dict(out=P(64))), (INVALID, dict(cfg=config(**H))),
+    (INVALID, dict(layers=(LAYER, KvqLayer(160, 16, 64, 48), LAYER))), (INVALID, dict(layers=(LAYER, KvqLayer(160, 16, 32, 48)))),
     (INVALID, dict(layers=(LAYER, KvqLayer(16, 16, None, 48)))), (UNSUPPORTED, dict(cfg=config(**WINDOW))),
     (CAPACITY, dict(max_len=249)), (ALIGN, dict(layers=(KvqLayer(24, 16, 32, 48),)))])
 def test_commit_refuses(want, over):

@@ -168,6 +168,22 @@ def test_rope_append_in_place_keys_only_and_repeat(cuda_device):
     kvq.kvq_rope_append(cfg, c, r, table, q[:, :0], k[:, :0], v[:, :0], out[:, :0], i32([0, 9]), 9)   # no tokens
 
 
+@pytest.mark.parametrize("dh,hq,rot,layout,dtype", [
+    (128, 5, 24, kvq.KVQ_ROPE_HALF, torch.float16), (128, 9, 96, kvq.KVQ_ROPE_HALF, torch.float32),
+    (64, 17, 8, kvq.KVQ_ROPE_HALF, torch.bfloat16), (64, 3, 40, kvq.KVQ_ROPE_INTERLEAVED, torch.float32),
+    (128, 6, 128, kvq.KVQ_ROPE_HALF, torch.bfloat16)])
+def test_rope_append_in_place_equals_apart(cuda_device, dh, hq, rot, layout, dtype):
+    gen = torch.Generator().manual_seed(rot)
+    cfg = make_cfg("k8v8", 3, 256, hq, 1, dh)
+    r = RopeConfig(rot, layout=layout)
+    table = kvq.kvq_rope_table(r, 300)
+    q, k, v = (torch.randn(3, 70, h, dh, generator=gen).to(dtype).cuda() for h in (hq, 1, 1))
+    a, b, out, same = make_layer(cfg, gen), make_layer(cfg, gen), torch.empty_like(q), q.clone()
+    kvq.kvq_rope_append(cfg, a, r, table, q, k, v, out, i32([0, 100, 9]), 100)
+    kvq.kvq_rope_append(cfg, b, r, table, same, k, v, same, i32([0, 100, 9]), 100)
+    assert torch.equal(out, same) and not torch.equal(out, q)
+
+
 @pytest.mark.parametrize("n", [5, 40])
 def test_rope_append_sliding_window(cuda_device, n):
     """Ring slots, with more tokens than the ring holds in one call (n = 40 > 24)."""

@@ -109,6 +109,27 @@ def test_ragged_trees_and_lengths(cuda_device, num_ctas):
     check(cfg, layer, q, lens, n_tree, masks, out)
 
 
+@pytest.mark.parametrize("fmt,dh,G,T,num_ctas,q_dtype", [
+    ("k8v8", 128, 1, 1, 4, F16), ("k8v8", 64, 3, 3, 5, BF16), ("k4v4g32", 128, 5, 7, 3, F16), ("k16v16", 128, 3, 23, 4, F32),
+    ("k8v8g32", 128, 1, 33, 2, BF16), ("asym", 64, 8, 9, 3, F32), ("tensor", 128, 5, 13, 1, F16), ("e4m3", 128, 2, 64, 6, F32)])
+def test_segments_of_many_tiles_shared_by_ctas(cuda_device, fmt, dh, G, T, num_ctas, q_dtype):
+    """Row tiles of several token tiles, some whole, some cut between CTAs (first and last partial of
+    a CTA among them); odd numbers of rows; scores that grow along the sequence, so that the running
+    maximum moves more than once."""
+    B, hkv, lens, cap = 3, 2, [700, 850, 333], 1024
+    gen = torch.Generator().manual_seed(13)
+    cfg = make_cfg(fmt, B, cap, hkv * G, hkv, dh)
+    layer = make_layer(cfg, gen)
+    k, v = (torch.randn(B, cap, hkv, dh, generator=gen) for _ in range(2))
+    k *= torch.linspace(0.1, 8.0, cap)[None, :, None, None]
+    kvq.kvq_append(cfg, layer, k.cuda(), v.cuda(), i32([0] * B), 0, cap)
+    q = torch.randn(B, T, hkv * G, dh, generator=gen).to(q_dtype).cuda()
+    n_tree = [T, max(T - 1, 1), T]
+    masks = random_masks(np.random.default_rng(13), B, T)
+    out = run_tree(cfg, layer, q, lens, n_tree, masks, F32, num_ctas=num_ctas)
+    check(cfg, layer, q, lens, n_tree, masks, out)
+
+
 def test_masks_causal_empty_dense_and_stray_bits(cuda_device):
     B, T, G, hkv, cap = 3, 64, 2, 1, 256
     lens = [0, 130, 64]
@@ -259,6 +280,76 @@ def test_stream_graphs_and_repeats(cuda_device):
     graphs[0].replay()
     torch.cuda.synchronize()
     check(cfg, layer, q, [5, 1000, 0], None, masks, outs[0])
+
+
+def test_two_streams_with_a_workspace_each(cuda_device):
+    B, T, G, hkv, cap = 4, 13, 4, 2, 1024
+    gen = torch.Generator().manual_seed(16)
+    cfg = make_cfg("k8v4g32", B, cap, hkv * G, hkv, 128)
+    layers = [filled(cfg, gen) for _ in range(2)]
+    q = torch.randn(B, T, hkv * G, 128, generator=gen).half().cuda()
+    d_len = i32([1000, 3, 640, 511])
+    want = [run_tree(cfg, x, q, [1000, 3, 640, 511], None, None, F16) for x in layers]
+    outs, wss = [torch.zeros_like(q) for _ in layers], [TreeWorkspace(cfg, T) for _ in layers]
+    streams = [torch.cuda.Stream() for _ in layers]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for x, o, ws, st in zip(layers, outs, wss, streams):
+            kvq.kvq_tree_attn(cfg, x, q, d_len, 1000, None, o, ws, stream=st)
+    torch.cuda.synchronize()
+    for o, w, ws in zip(outs, want, wss):
+        assert torch.equal(o, w) and kvq.kvq_workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_a_captured_step_equals_the_eager_one(cuda_device, paged):
+    """Rotation and append, tree attention, commit and reading back in one graph, replayed on other
+    inputs in the same buffers."""
+    B, T, G, hkv, dh, cap = 3, 11, 3, 2, 128, 384
+    gen = torch.Generator().manual_seed(17)
+    cfg = make_cfg("k8v8", B, cap, hkv * G, hkv, dh, n_pages=B * cap // 128 + 2 if paged else 0)
+    rope = kvq.RopeConfig(dh)
+    table = kvq.kvq_rope_table(rope, cap)
+    layers = [make_layer(cfg, gen) for _ in range(2)]
+    for x in layers[1:]:                                        # both start with the same cache
+        for name in ("k_codes", "k_scales", "v_codes", "v_scales", "block_table"):
+            if getattr(x, name) is not None:
+                getattr(x, name).copy_(getattr(layers[0], name))
+
+    def buffers():
+        return dict(qkv=torch.zeros(B, T, hkv * (G + 2), dh, dtype=F16, device="cuda"), d_len=i32([0] * B), n=i32([0] * B),
+                    path=i32([[0, 2, 5]] * B), m=i32([0] * B), q=torch.zeros(B, T, hkv * G, dh, dtype=F16, device="cuda"),
+                    out=torch.zeros(B, T, hkv * G, dh, dtype=F16, device="cuda"), new=i32([0] * B),
+                    k=torch.zeros(B, 3, hkv, dh, device="cuda"), ws=TreeWorkspace(cfg, T))
+
+    def step(layer, s):
+        q, k, v = s["qkv"].split([hkv * G, hkv, hkv], dim=2)
+        kvq.kvq_rope_append(cfg, layer, rope, table, q, k, v, s["q"], s["d_len"], cap - T, d_count=s["n"])
+        kvq.kvq_tree_attn(cfg, layer, s["q"], s["d_len"], cap - T, None, s["out"], s["ws"], d_n_tree=s["n"])
+        kvq.kvq_tree_commit(cfg, [layer], s["d_len"], cap - T, s["path"], s["m"], T, d_len_out=s["new"])
+        kvq.kvq_read(cfg, layer, s["k"], None, s["d_len"], cap - T, d_count=s["m"])
+
+    a, b = buffers(), buffers()
+    step(layers[1], b)                                          # no tokens: loads the kernels, changes nothing
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=side):
+        step(layers[1], b)
+    for lens, n, m in (([0, 130, 1], [11, 7, 0], [3, 2, 0]), ([3, 132, 1], [11, 11, 9], [0, 3, 1])):
+        qkv = torch.randn(B, T, hkv * (G + 2), dh, generator=gen).half()
+        for s in (a, b):
+            s["qkv"].copy_(qkv)
+            for name, x in (("d_len", lens), ("n", n), ("m", m)):
+                s[name].copy_(i32(x))
+        step(layers[0], a)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for name in ("q", "out", "new", "k"):
+            assert torch.equal(a[name], b[name]), name
+        assert a["new"].tolist() == [x + y for x, y in zip(lens, m)]
+        for x, y in zip(logical(layers[0], cfg), logical(layers[1], cfg)):
+            assert np.array_equal(x, y)
 
 
 def test_guard_bytes_around_out_and_workspace(cuda_device):
