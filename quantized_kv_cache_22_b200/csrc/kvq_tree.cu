@@ -11,25 +11,41 @@
 // row tile inside a CTA is a segment.  A segment that is the whole row tile writes the output,
 // others leave (sum, max, l) partials that tree_merge_kernel joins.
 //
-// Per tile.
-//   * A producer thread copies the raw codes and scales (contiguous in either layout: one bulk
+// Roles of a CTA's 20 warps; nothing but barriers passes between them, each walks the segments
+// by itself.
+//   * A producer thread copies raw codes and scales (contiguous in either layout: one bulk
 //     copy each) into a ring whose entries hold one tile of K or of V.
-//   * Eight converter warps turn codes into f16 operands in 128-byte-swizzled shared memory:
-//     every code (INT8, INT4, e4m3, code minus zero-point) is exact in f16.  One scale per row
-//     stays outside the product.  Scales per group go in as x = code * (scale / 2^e) in two
-//     f16 parts, hi = rn(x) and lo = x - hi (both exact: at most 8 + 11 significant bits), 2^e
-//     being the power of two of the row's largest scale; the product then takes both parts.
-//   * S = Q K^T: tcgen05.mma kind::f16, M = 128 rows, N = 128 tokens; Q in TMEM (rows scaled by
-//     a power of two, fp32 rows in two parts), K from shared memory, fp32 accumulators in TMEM.
-//   * Softmax: a thread owns a row.  z = s * scale_k + log2(scale_v) in log2 units, so that
-//     P = 2^(z - m) is the probability times the value scale, rounded to f16 (the only
-//     rounding below fp32 in the path; m keeps P between the subnormals and 2^14), and
-//     l += P / scale_v.  m moves only when P would pass 2^14: then O in TMEM is rescaled.
-//   * O += P V: A = P in TMEM (over S's columns), B = V, MN-major.
+//   * Four warps turn K's codes, four V's, into f16 operands in 128-byte-swizzled shared
+//     memory: every code (INT8, INT4, e4m3, code minus zero-point) is exact in f16.  One scale
+//     per row stays outside the product.  Scales per group go in as x = code * (scale / 2^e) in
+//     two f16 parts, hi = rn(x) and lo = x - hi (both exact: at most 8 + 11 significant bits),
+//     2^e being the power of two of the row's largest scale; the product then takes both parts.
+//   * One warp issues the products.  S = Q K^T: M = 128 rows, N = 128 tokens, A = Q in TMEM
+//     (rows scaled by a power of two, fp32 rows in two parts), B = K, fp32 accumulators in TMEM,
+//     S of even and of odd tiles apart.  O += P V: A = P in TMEM, B = V, MN-major.  (A from TMEM
+//     takes 74 clocks a K step of 16 at N = 128, A from shared memory 107.)  The order is
+//     S(i + 2), P V(i), so that the scores are two tiles ahead.
+//   * Two softmax groups of four warps take the tiles in turns: a thread owns a TMEM lane.
+//     z = s * scale_k + log2(scale_v) in log2 units, so that P = 2^(z - m) is the probability
+//     times the value scale, rounded to f16 (the only rounding below fp32 in the path: the
+//     product's other operand is f16 too; m keeps P between the subnormals and 2^14), and
+//     l += P / scale_v in fp32.  O and m are common to both groups.  m moves only when a P would
+//     pass 2^14; then O in TMEM is rescaled between two tiles' products, and a P that was made
+//     with the older m is scaled by the power of two before it goes out.
 //   * Few rows: with at most 64 (32) rows Q is laid into TMEM two (four) times, and each copy's
 //     warps take one half (quarter) of the tile's tokens with zeros in the rest of their P, so
 //     that all four warps share the exponentials; the copies' sums are joined at the end.
-// Double-buffered S and P let the tensor cores run a tile ahead of the softmax.
+//
+// What bounds it.  16 x 8192 tokens of 8 KV heads, INT8, 4 heads a group: 118 us with 16 drafted
+// tokens (64 rows a KV head; its bytes alone would take 42), 285 with 64 (two row tiles, every
+// tile converted for both; the products alone 86): a tile of 128 tokens takes 3500 cycles, of
+// which the tensor cores work 1200, the issue slots 1900 (conversion of 32 thousand codes, 16
+// thousand exponentials); the rest is the chain scores - softmax - product of a tile, through
+// three barriers of 100 cycles and more each.  One group of softmax warps instead of two took
+// 25% longer, converter warps that serve K and V in turns 10%.  Short segments pay the opening
+// of a row tile and its output (8 to 12 thousand cycles, code and constants fetched cold): 64
+// sequences of 4000 tokens, INT4 in pages, 8 drafted, 160 us; 8 ragged ones of up to 2011, K
+// INT8 and V INT4 in groups of 32, 24 drafted, 49 us.
 //
 // Every wait is bounded; a give-up records KVQ_ERR_TIMEOUT in the workspace's status word.
 #include <algorithm>
@@ -52,7 +68,7 @@ constexpr unsigned FULL = 0xffffffffu;
 
 // Registers a thread: the block starts with 96 x 640 threads and shares them out anew by
 // warpgroup (2 x softmax, producer and issuer, 2 x converters: 480 in all, as launched).
-constexpr int kSoftRegs = 144, kIssueRegs = 48, kConvRegs = 72;
+constexpr int kSoftRegs = 144, kIssueRegs = 64, kConvRegs = 64;
 static_assert(2 * kSoftRegs + kIssueRegs + 2 * kConvRegs == 5 * 96, "the shares add up to the launch");
 template <int N>
 __device__ __forceinline__ void more_regs() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -747,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         // m is raised in a second pass over the tile, when some token would not fit; O is then
         // rescaled between the two tiles' P V, with no other P in flight.
         auto tiles = [&](auto ch, int i0, int count) {
-            constexpr int CH = decltype(ch)::value, N = CH == 4 ? 16 : 32;   // (tokens at a time: registers)
+            constexpr int CH = decltype(ch)::value, N = 32;
 #pragma unroll 1
             for (int k = (i0 ^ grp) & 1; k < count; k += 2) {
                 i = i0 + k;
@@ -777,10 +793,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                         uint64_t z[N / 2];
                         tmem_ld_async(s_at + c, a);
                         tmem_ld_wait(a);
-                        const uint32_t vis = whole ? FULL : visible(t0 + c, it.s.len, row.mask) | (N == 32 ? 0u : 0xffff0000u);
+                        const uint32_t vis = whole ? FULL : visible(t0 + c, it.s.len, row.mask);
                         const float mx = scores<N>(a, sk + c, lv + c, row.rf, vis, z);
                         fits = fits && (!(mx > m + kMoveAt) || mx == -INFINITY);
-                        sum += probs<N>(z, iv + c, me, *reinterpret_cast<uint32_t(*)[N / 2]>(&pw[0][0] + c / 2));
+                        sum += probs<N>(z, iv + c, me, pw[c / N]);
                     }
                     if (second || __builtin_expect(__all_sync(FULL, fits), 1)) break;
                     // ---- the tile's maximum, then m, O and l after it
@@ -859,12 +875,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 #pragma unroll 1
         while (it.count) {
             const int i0 = i, copies = row.copies, count = opened ? it.count : 0;
-            if (copies == 4)
-                tiles(Int<1>(), i0, count);
+            if (copies == 1)
+                tiles(Int<4>(), i0, count);
             else if (copies == 2)
                 tiles(Int<2>(), i0, count);
             else
-                tiles(Int<4>(), i0, count);
+                tiles(Int<1>(), i0, count);
             i = i0 + count;
             // ---- the next segment's queries come in, by the group of its first tile, once this
             // one's scores are all done; the other group has read its S
