@@ -35,17 +35,20 @@
 //   * Few rows: with at most 64 (32) rows Q is laid into TMEM two (four) times, and each copy's
 //     warps take one half (quarter) of the tile's tokens with zeros in the rest of their P, so
 //     that all four warps share the exponentials; the copies' sums are joined at the end.
+//     (64 rows: 119 us against 145 without copies; 32 rows: 160 against 266.)
 //
 // What bounds it.  16 x 8192 tokens of 8 KV heads, INT8, 4 heads a group: 118 us with 16 drafted
 // tokens (64 rows a KV head; its bytes alone would take 42), 285 with 64 (two row tiles, every
-// tile converted for both; the products alone 86): a tile of 128 tokens takes 3500 cycles, of
-// which the tensor cores work 1200, the issue slots 1900 (conversion of 32 thousand codes, 16
-// thousand exponentials); the rest is the chain scores - softmax - product of a tile, through
-// three barriers of 100 cycles and more each.  One group of softmax warps instead of two took
-// 25% longer, converter warps that serve K and V in turns 10%.  Short segments pay the opening
-// of a row tile and its output (8 to 12 thousand cycles, code and constants fetched cold): 64
-// sequences of 4000 tokens, INT4 in pages, 8 drafted, 160 us; 8 ragged ones of up to 2011, K
-// INT8 and V INT4 in groups of 32, 24 drafted, 49 us.
+// tile converted for both; the products alone 84).  With 16, a tile of 128 tokens takes 3500
+// cycles, of which the tensor cores work 1200 and the issue slots 1900 (conversion of 32
+// thousand codes, 8 thousand exponentials); the rest is the chain scores - softmax - product of
+// a tile, through three barriers of 100 cycles and more each.  Steps that measured well: K and V
+// converted by warps of their own, 199 -> 144 us; two softmax groups, 144 -> 137; P in columns of
+// its own and whole query rows in one load, 130 -> 125; a tile's scores in one product instead of
+// two, 125 -> 113.  Groups that take tiles in turns instead of halves of each made short segments
+// 5% faster.  A segment pays the opening of its row tile and its output, 8 to 12 thousand cycles
+// with code and constants fetched cold: 64 sequences of 4000 tokens, INT4 in pages, 8 drafted,
+// 160 us; 8 ragged ones of up to 2011, K INT8 and V INT4 in groups of 32, 24 drafted, 49 us.
 //
 // Every wait is bounded; a give-up records KVQ_ERR_TIMEOUT in the workspace's status word.
 #include <algorithm>
@@ -943,7 +946,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             if (direct) f = L != 0.f ? f / L : 0.f;
             if (!direct && ok && threadIdx.x < rows) *reinterpret_cast<float2 *>(part_ml) = make_float2(M, L);
             if (copies == 1) {
-                // every thread has a row's sums: half of its columns, 16 a time
+                // every thread has a row's sums: half of its columns, 16 a time (through the
+                // staging below 8 x 2011 tokens, 72 rows, took 52.4 us, so 50.8)
                 const int64_t at = (direct ? row_at(place) : (int64_t)place * DH) + DH / 2 * grp;
 #pragma unroll 1
                 for (int c = 0; c < DH / 2; c += 16) {
@@ -1155,7 +1159,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-// One warp joins the partials of one row whose row tile several CTAs shared.
+// One warp joins the partials of one row whose row tile several CTAs shared: bound by latency
+// (the row tile's entry, the maxima, then the sums), 4 to 14 us apart from the kernel before,
+// most of it launch and cold fetches.
 template <int DH>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeParams p)
 {
