@@ -39,8 +39,8 @@
 //
 // What bounds it.  16 x 8192 tokens of 8 KV heads, INT8, 4 heads a group: 118 us with 16 drafted
 // tokens (64 rows a KV head; its bytes alone would take 42), 285 with 64 (two row tiles, every
-// tile converted for both; the products alone 84).  With 16, a tile of 128 tokens takes 3500
-// cycles, of which the tensor cores work 1200 and the issue slots 1900 (conversion of 32
+// tile converted for both; the products alone 84).  With 16, a tile of 128 tokens takes 3400
+// cycles, of which the tensor cores work 1000 and the issue slots 1500 (conversion of 32
 // thousand codes, 8 thousand exponentials); the rest is the chain scores - softmax - product of
 // a tile, through three barriers of 100 cycles and more each.  Steps that measured well: K and V
 // converted by warps of their own, 199 -> 144 us; two softmax groups, 144 -> 137; P in columns of
