@@ -54,7 +54,7 @@ __device__ __forceinline__ void codes_of(const float (&x)[8], float s, float inv
 }
 
 // Quantise a row that LPR lanes hold, lane t elements 8t .. 8t+7 (v[0]) and DH/2 + 8t .. (v[1]),
-// as quantize4 does: the same codes and scales bit for bit.
+// as quantize_row does: the same codes and scales bit for bit.
 template <int DH>
 __device__ __forceinline__ void quantize_row16(const float (&v)[2][8], bool active, int t, int bits, int gshift, int fmt,
                                                uint8_t *codes, __half *scales)
