@@ -516,8 +516,11 @@ KVQ_API int kvq_read(const kvq_config *cfg, const kvq_layer *layer, const kvq_ro
  * KV head h / G:
  *   s_t = softmax_scale * q . k^_t,  p = softmax(s) over the attended t,  out = sum p_t v^_t
  * with codes and scales exact, and fp32 scores, sums and accumulators; the probabilities
- * enter the second product as p_t * (value scale) rounded to fp16 (relative error 2^-11 a
- * token).  A row that attends nothing gets zeros; rows i >= n are left as they were.
+ * enter the second product as p_t * (value scale) rounded to fp16: each is off by 2^-11 of
+ * itself, or by 2^-30 of the row's largest p_t * scale where that is more.  A token whose
+ * value scale is zero (its codes are zeros, as every append writes them) counts in the sum of
+ * the probabilities only.  A row that attends nothing gets zeros; rows i >= n are left as
+ * they were.
  * Masked places do not reach a row, whatever they hold; a row that attends a non-finite
  * key or value gets an unspecified result.
  *   q        device [B][n_tree][Hq][Dh], q_dtype KVQ_F16, KVQ_F32 or KVQ_BF16; G <= 8

@@ -277,10 +277,18 @@ struct Walk {
 };
 
 // ------------------------------------------------------------------ codes to f16
+// log2 of what a value row whose scales are all zero gets for a scale: the token counts in the sum
+// of the probabilities, but its P, which brings nothing, must not set m, or the others' P would fall
+// among f16's subnormals.  Its codes are zeros too, as every append writes them; others would count
+// 2^-64 each.  (Zeros in the operand instead took 2 to 10 % longer; and with a lower number ex2
+// would flush a P to zero that l still needs.)
+constexpr int kZeroRow = -64;
+
 // Scales of one token as the converters see them.
 struct RowScale {
     int e;        // exponent of the largest group scale (grouped)
     bool bad;     // a scale or zero-point that is not a finite number
+    bool zero;    // every scale is zero
 };
 template <int KIND>
 __device__ __forceinline__ RowScale row_scale(const uint16_t *sc, int t, int ng)
@@ -294,6 +302,7 @@ __device__ __forceinline__ RowScale row_scale(const uint16_t *sc, int t, int ng)
     RowScale r;
     r.bad = m >= 0x7c00 || z > 0x5bf8;              // 0x5bf8: 255
     r.e = m >= 0x400 ? (m >> 10) - 15 : -14;
+    r.zero = m == 0;
     return r;
 }
 
@@ -307,8 +316,9 @@ __device__ __forceinline__ void token_numbers(const uint16_t *sc, int t, bool ba
     if constexpr (GRP) {
         const RowScale r = row_scale<KIND>(sc, t, ng);
         if constexpr (ISV) {
-            p0[t] = bad || r.bad ? __int_as_float(0x7fc00000) : (float)r.e;
-            p1[t] = pow2i(-r.e);
+            const int e = r.zero ? kZeroRow : r.e;
+            p0[t] = bad || r.bad ? __int_as_float(0x7fc00000) : (float)e;
+            p1[t] = pow2i(-e);
         } else {
             p0[t] = pow2i(r.e);
         }
@@ -319,9 +329,10 @@ __device__ __forceinline__ void token_numbers(const uint16_t *sc, int t, bool ba
         if constexpr (ISV) {
             s = fabsf(s);
             if (!(s < INFINITY)) bad = true;
-            // every value of the row is zero, or nothing may come of it (the inverse meets
-            // P = 0 where the token is masked, so it has to be a number)
-            if (s == 0.f || bad || t >= nvalid) s = 1.f;
+            // nothing may come of the token (the inverse meets P = 0 where it is masked, so it has
+            // to be a number)
+            if (bad || t >= nvalid) s = 1.f;
+            if (s == 0.f) s = pow2i(kZeroRow);
             p0[t] = bad ? __int_as_float(0x7fc00000) : lg2(s);
             p1[t] = __fdividef(1.f, s);
         } else {
@@ -639,7 +650,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         const uint32_t s_row = tmem + COL_S + 128u * grp + lane_off, o_row = tmem + COL_O + lane_off;
         const uint32_t p_row = over ? s_row : tmem + COL_P + lane_off;
         float4 *stage = reinterpret_cast<float4 *>(smem + keep(p.l.off_stage));
-        const float osign = p.fmt == KVQ_FMT_TENSOR && __half2float(p.v.scales[0]) < 0.f ? -1.f : 1.f;
+        float osign = 1.f;
+        if (p.fmt == KVQ_FMT_TENSOR) {
+            const float s = __half2float(p.v.scales[0]);
+            osign = s < 0.f ? -1.f : s == 0.f ? 0.f : 1.f;
+        }
         // A wait that gave up does not end the role: the eight warps meet at a hardware barrier
         // at every segment's end, so all of them walk on to the end (with the abort flag up no
         // further wait takes time) and write nothing more.
