@@ -861,14 +861,22 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 tc_fence_after();
                 const float then = ctl->m[place];
                 if (__builtin_expect(__any_sync(FULL, then != m), 0)) {
-                    const float alpha = m == then ? 1.f : ex2(m - then);
-                    const uint32_t alpha2 = pack_half2(alpha, alpha);
-                    l *= alpha;
+                    // a power of two, in two factors: f16 holds them down to 2^-24 (of a P below 2^14
+                    // nothing is left beyond 2^-48, and an m of -inf has left zeros)
+                    float d = m == then ? 0.f : m - then;
+                    l *= ex2(d);
                     m = then;
+                    d = fmaxf(d, -48.f);
+#pragma unroll 1
+                    for (int k2 = 0; k2 < 2; k2++) {
+                        const float alpha = ex2(fmaxf(d, -24.f));
+                        const uint32_t alpha2 = pack_half2(alpha, alpha);
+                        d -= fmaxf(d, -24.f);
 #pragma unroll
-                    for (int c = 0; c < CH; c++)
+                        for (int c = 0; c < CH; c++)
 #pragma unroll
-                        for (int q = 0; q < 16; q++) pw[c][q] = hmul2_u32(pw[c][q], alpha2);
+                            for (int q = 0; q < 16; q++) pw[c][q] = hmul2_u32(pw[c][q], alpha2);
+                    }
                 }
 #pragma unroll
                 for (int c = 0; c < CH; c++) tmem_st16(p_at + 16u * c, pw[c]);

@@ -178,3 +178,30 @@ def test_a_tensor_scale_of_zero(cuda_device):
     q = torch.randn(B, T, hkv * G, 128, generator=gen).half().cuda()
     for ctas in (1, 3):
         assert torch.all(run_tree(cfg, layer, q, [L], None, num_ctas=ctas) == 0)
+
+
+# ----------------------------------------------------------------------------- a maximum that jumps
+
+def test_a_tile_far_below_a_later_maximum_still_counts(cuda_device):
+    """The tile after the one that raises the maximum by more than 2^24: its tokens are 2^-17.6 of the
+    largest each, and the only ones with a value in most columns."""
+    B, T, G, hkv, dh, cap, L = 1, 64, 2, 1, 64, 512, 384
+    gen = torch.Generator().manual_seed(35)
+    cfg = make_cfg("k8v8", B, cap, hkv * G, hkv, dh)
+    layer = make_layer(cfg, gen)
+    log2_score = torch.zeros(cap)
+    log2_score[:128] = 6.0
+    log2_score[128 + 40] = 31.5
+    log2_score[256:384] = 13.9
+    k, v = torch.zeros(B, cap, hkv, dh), torch.zeros(B, cap, hkv, dh)
+    k[0, :, 0, 0] = log2_score
+    v[0, :, 0, 0] = 1.0
+    v[0, 256:384, 0] = torch.rand(128, dh, generator=gen) + 0.01
+    v[0, 256:384, 0, 0] = 1.0
+    append(cfg, layer, k, v)
+    q = torch.zeros(B, T, hkv * G, dh)
+    q[..., 0] = math.log(2) * math.sqrt(dh)
+    q = q.half().cuda()
+    for ctas in (1, 2):
+        out = run_tree(cfg, layer, q, [L], None, num_ctas=ctas)
+        check(cfg, layer, q, [L], None, out)
