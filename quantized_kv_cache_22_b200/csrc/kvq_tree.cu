@@ -775,7 +775,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         float m = -INFINITY, l = 0.f;                // the group's: l in units of 2^m
         int i = 0;                                   // units done
         // P of tile i, CH times 32 tokens a thread.
-        // The probabilities are made in registers, with the m that stands when the tile begins.
+        // The probabilities are made in registers, with the m that the group's tile before ended with
+        // (the other group may have raised it already or not: bits must not depend on that).
         // P's columns are free, and m is final up to this tile, once P V of the tile before is
         // done: then P goes out, scaled again if the other group has raised m meanwhile.
         // m is raised in a second pass over the tile, when some token would not fit; O is then
@@ -792,11 +793,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 const uint32_t s_at = s_row + (uint32_t)row.tb, p_at = p_row + (uint32_t)row.tb / 2;
                 uint32_t pw[CH][16];
                 float sum;
-                const float now = ctl->m[place];
-                if (now != m) {
-                    l *= ex2(m - now);
-                    m = now;
-                }
                 hold(&ctl->sfull[j], i >> 1);
                 hold(&ctl->par[i & 3], i >> 2);
                 tc_fence_after();

@@ -205,3 +205,36 @@ def test_a_tile_far_below_a_later_maximum_still_counts(cuda_device):
     for ctas in (1, 2):
         out = run_tree(cfg, layer, q, [L], None, num_ctas=ctas)
         check(cfg, layer, q, [L], None, out)
+
+
+# ----------------------------------------------------------------------------- whatever the timing
+
+@pytest.mark.parametrize("T,G,num_ctas", [(64, 2, 4), (12, 4, 4), (5, 3, 7), (64, 8, 0)])
+def test_the_same_bits_whatever_the_timing(cuda_device, T, G, num_ctas):
+    """Every second tile raises the maximum, by one group of softmax warps, while the other has the
+    next tile in hand: a call's bits do not depend on which of them is ahead."""
+    B, hkv, dh, cap, lens = 4, 2, 128, 4096, [4000, 3333, 4000, 2048]
+    gen = torch.Generator().manual_seed(36)
+    cfg = make_cfg("k8v8", B, cap, hkv * G, hkv, dh)
+    layer = make_layer(cfg, gen)
+    u = torch.randn(dh, generator=gen).sign()
+    k, v = (torch.randn(B, cap, hkv, dh, generator=gen) for _ in range(2))
+    tile = torch.arange(cap) // 128
+    level = torch.where(tile % 2 == 1, (tile + 1) * 10.0, tile * 10.0 - 14.0)      # of the scores, log2
+    k += (level * math.log(2) / math.sqrt(dh))[None, :, None, None] * u
+    append(cfg, layer, k, v)
+    q = (u + 0.2 * torch.randn(B, T, hkv * G, dh, generator=gen)).half().cuda()
+    masks = random_masks(np.random.default_rng(36), B, T)
+    ws = TreeWorkspace(cfg, T, num_ctas)
+    first = run_tree(cfg, layer, q, lens, masks, num_ctas, ws=ws)
+    # another stream's work moves the warps against one another
+    other, busy = torch.cuda.Stream(), torch.randn(2048, 2048, device="cuda")
+    d_len, d_mask, outs = i32(lens), mask_tensor(masks), [torch.empty_like(first) for _ in range(60)]
+    torch.cuda.synchronize()
+    for o in outs:
+        with torch.cuda.stream(other):
+            busy @ busy
+        kvq.kvq_tree_attn(cfg, layer, q, d_len, 4000, d_mask, o, ws, num_ctas=num_ctas)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, first) for o in outs)
+    assert kvq.kvq_workspace_status(ws) == 0
