@@ -515,7 +515,9 @@ KVQ_API int kvq_read(const kvq_config *cfg, const kvq_layer *layer, const kvq_ro
  * and j < n; d_mask NULL selects the causal mask j <= i (a chain).  For query head h of
  * KV head h / G:
  *   s_t = softmax_scale * q . k^_t,  p = softmax(s) over the attended t,  out = sum p_t v^_t
- * with codes and scales exact, and fp32 scores, sums and accumulators; the probabilities
+ * with codes exact, scales exact (those of a row's groups while they are within 2^20 of the
+ * row's largest; below that, and for e4m3 codes, an element may be off by 2^-31 of the row's
+ * largest), and fp32 scores, sums and accumulators; the probabilities
  * enter the second product as p_t * (value scale) rounded to fp16: each is off by 2^-11 of
  * itself, or by 2^-30 of the row's largest p_t * scale where that is more.  A token whose
  * value scale is zero (its codes are zeros, as every append writes them) counts in the sum of

@@ -18,8 +18,11 @@
 //   * Four warps turn K's codes, four V's, into f16 operands in 128-byte-swizzled shared
 //     memory: every code (INT8, INT4, e4m3, code minus zero-point) is exact in f16.  One scale
 //     per row stays outside the product.  Scales per group go in as x = code * (scale / 2^e) in
-//     two f16 parts, hi = rn(x) and lo = x - hi (both exact: at most 8 + 11 significant bits),
-//     2^e being the power of two of the row's largest scale; the product then takes both parts.
+//     two f16 parts, hi = rn(x) and lo = x - hi (at most 8 + 11 significant bits), 2^e being a power
+//     of two that brings the row's largest scale near f16's upper end; the product then takes both
+//     parts.  Both are exact while a group's scale is within 2^21 of the row's largest (INT8 2^22,
+//     INT4 2^26); below that its values are off by 2^-31 of the row's largest value at most.  e4m3's
+//     small codes, whose last bit lies at 2^-9, are off by 2^-31 of the row's largest scale.
 //   * One warp issues the products.  S = Q K^T: M = 128 rows, N = 128 tokens, A = Q in TMEM
 //     (rows scaled by a power of two, fp32 rows in two parts), B = K, fp32 accumulators in TMEM,
 //     S of even and of odd tiles apart.  O += P V: A = P in TMEM, B = V, MN-major.  (A from TMEM
@@ -290,6 +293,12 @@ struct RowScale {
     bool bad;     // a scale or zero-point that is not a finite number
     bool zero;    // every scale is zero
 };
+// Groups' factors scale / 2^e are raised by 2^kRaise, the most that keeps code * factor within f16
+// (8 * 2^13, 127 * 2^9, 255 * 2^8, 448 * 2^7): a group whose scale is up to 2^(14 + kRaise) below its
+// row's largest still has a normal f16 number for its factor.
+template <int KIND>
+constexpr int kRaise = KIND == K_INT4 ? 12 : KIND == K_INT8 ? 8 : KIND == K_ASYM ? 7 : 6;
+
 template <int KIND>
 __device__ __forceinline__ RowScale row_scale(const uint16_t *sc, int t, int ng)
 {
@@ -316,11 +325,11 @@ __device__ __forceinline__ void token_numbers(const uint16_t *sc, int t, bool ba
     if constexpr (GRP) {
         const RowScale r = row_scale<KIND>(sc, t, ng);
         if constexpr (ISV) {
-            const int e = r.zero ? kZeroRow : r.e;
+            const int e = r.zero ? kZeroRow : r.e - kRaise<KIND>;
             p0[t] = bad || r.bad ? __int_as_float(0x7fc00000) : (float)e;
             p1[t] = pow2i(-e);
         } else {
-            p0[t] = pow2i(r.e);
+            p0[t] = pow2i(r.e - kRaise<KIND>);
         }
     } else {
         float s = 1.f;
@@ -395,7 +404,7 @@ __device__ __forceinline__ void convert(const uint8_t *raw, const uint16_t *sc, 
             uint8_t *d = out + u * RPP * 128 + panel * PANEL;
             if constexpr (GRP) {
                 const RowScale rs = row_scale<KIND>(sc, t, ng);
-                float s = __half2float(__ushort_as_half(sc[(t * ng + g) * PAIR])) * pow2i(-rs.e);
+                float s = __half2float(__ushort_as_half(sc[(t * ng + g) * PAIR])) * pow2i(kRaise<KIND> - rs.e);
                 if (ISV && rs.bad) s = 0.f;
                 const uint32_t s2 = pack_half2(s, s);
                 uint32_t l[4];

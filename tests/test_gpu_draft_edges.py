@@ -238,3 +238,29 @@ def test_the_same_bits_whatever_the_timing(cuda_device, T, G, num_ctas):
     torch.cuda.synchronize()
     assert all(torch.equal(o, first) for o in outs)
     assert kvq.kvq_workspace_status(ws) == 0
+
+
+# ----------------------------------------------------------------------------- groups that lie far apart
+
+@pytest.mark.parametrize("which,fmt,dh", [
+    (which, fmt, dh) for which in "kv" for fmt, dh in (
+        ("k8v8g32", 128), ("k8v8g32", 64), ("k4v4g32", 64), ("e4m3g32", 128), ("asymg32", 128), ("asymg32", 64))]
+    + [("k", "k4g32v8", 128), ("v", "k8v4g32", 128)])
+def test_a_small_group_beside_a_large_one(cuda_device, which, fmt, dh):
+    """One group's scale 2^18 times the others': their columns of the output, and scores that come from
+    them alone, are as exact as any."""
+    B, T, G, hkv, cap, L = 1, 9, 4, 1, 384, 333
+    gen = torch.Generator().manual_seed(37)
+    cfg = make_cfg(fmt, B, cap, hkv * G, hkv, dh)
+    layer = make_layer(cfg, gen)
+    k, v = (torch.randn(B, cap, hkv, dh, generator=gen) for _ in range(2))
+    q = torch.randn(B, T, hkv * G, dh, generator=gen)
+    if which == "k":
+        k[..., :32] *= 2.0 ** 18
+        q[..., :32] = 0.0
+    else:
+        v[..., :32] *= 2.0 ** 18
+    append(cfg, layer, k, v)
+    masks = random_masks(np.random.default_rng(37), B, T)
+    q = q.half().cuda()
+    check(cfg, layer, q, [L], masks, run_tree(cfg, layer, q, [L], masks))
