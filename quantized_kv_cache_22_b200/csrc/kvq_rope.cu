@@ -31,26 +31,29 @@ __global__ void __launch_bounds__(256) rope_table_kernel(const __grid_constant__
 // t: rne of the IEEE quotients x / s, plus z, clamped.  x * inv + 1.5 * 2^23 rounds the product
 // with the inverse to an integer; it is at most 2^-13 off the quotient (|x / s| < 2^8, above
 // that both are clamped), so away from the midpoints between integers both round alike.  Near
-// one (an element in 2500 is) the lane divides.
-__device__ __forceinline__ void codes_of(const float (&x)[8], float s, float inv, float z, float least, float most,
+// one (an element in 2500 is), and where an element or the scale is no finite number, the lane
+// divides and converts as quantize_row does.
+__device__ __forceinline__ void codes_of(const float (&x)[8], float s, float inv, int z, int least, int most,
                                          uint32_t (&t)[8])
 {
     constexpr float kRound = 12582912.f;
     // (a scale far below the values, a negative or an infinite one leave the inverse's range)
-    bool near = !(inv > 0.f);
+    bool far = inv > 0.f;
     float n[8];
 #pragma unroll
     for (int e = 0; e < 8; e++) {
         n[e] = fmaf(x[e], inv, kRound);
-        near |= fabsf(fmaf(x[e], inv, kRound - n[e])) > 0.4998f;
+        far &= fabsf(fmaf(x[e], inv, kRound - n[e])) <= 0.4998f;
     }
-    if (near && s != 0.f) {
+    if (!far && s != 0.f) {
 #pragma unroll
-        for (int e = 0; e < 8; e++) n[e] = rintf(__fdiv_rn(x[e], s)) + kRound;
+        for (int e = 0; e < 8; e++)      // (the sum wraps around where the quotient has saturated, as there)
+            t[e] = (uint32_t)max(least, min(most, (int)((uint32_t)__float2int_rn(__fdiv_rn(x[e], s)) + (uint32_t)z)));
+        return;
     }
 #pragma unroll
     for (int e = 0; e < 8; e++)
-        t[e] = s == 0.f ? 0u : __float_as_uint(fminf(fmaxf(n[e] + z, kRound + least), kRound + most));
+        t[e] = s == 0.f ? 0u : __float_as_uint(fminf(fmaxf(n[e] + (float)z, kRound + (float)least), kRound + (float)most));
 }
 
 // Quantise a row that LPR lanes hold, lane t elements 8t .. 8t+7 (v[0]) and DH/2 + 8t .. (v[1]),
@@ -76,7 +79,8 @@ __device__ __forceinline__ void quantize_row16(const float (&v)[2][8], bool acti
 #pragma unroll
     for (int h = 0; h < 2; h++) {
         lo[h] = 0.f;
-        hi[h] = 0.f;
+        // (maxima pass over NaN; a group of nothing else has a NaN scale)
+        hi[h] = fmt == KVQ_FMT_ASYM ? 0.f : fabsf(v[h][0]);
         if (fmt == KVQ_FMT_ASYM) {
 #pragma unroll
             for (int e = 0; e < 8; e++) {
@@ -85,7 +89,7 @@ __device__ __forceinline__ void quantize_row16(const float (&v)[2][8], bool acti
             }
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; e++) hi[h] = fmaxf(hi[h], fabsf(v[h][e]));
+            for (int e = 1; e < 8; e++) hi[h] = fmaxf(hi[h], fabsf(v[h][e]));
         }
     }
     if (joint) {
@@ -137,9 +141,9 @@ __device__ __forceinline__ void quantize_row16(const float (&v)[2][8], bool acti
         } else {
             uint32_t q[8];
             if (fmt == KVQ_FMT_ASYM)
-                codes_of(v[h], s, inv, (float)z, 0.f, 255.f, q);
+                codes_of(v[h], s, inv, z, 0, 255, q);
             else
-                codes_of(v[h], s, inv, 0.f, -qmax, qmax, q);
+                codes_of(v[h], s, inv, 0, -(int)qmax, (int)qmax, q);
 #pragma unroll
             for (int k = 0; k < 2; k++)
                 w[k] = __byte_perm(__byte_perm(q[4 * k], q[4 * k + 1], 0x0040), __byte_perm(q[4 * k + 2], q[4 * k + 3], 0x0040),

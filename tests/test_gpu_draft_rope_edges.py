@@ -1,0 +1,54 @@
+"""kvq_rope_append, kvq_rope_table and kvq_tree_commit at the edges of what their arguments may hold."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import quantized_kv_cache_22_b200 as kvq
+from quantized_kv_cache_22_b200 import LayerCache, RopeConfig
+from _draft import FORMATS, logical, make_cfg, make_layer, rotated
+from _helpers import to_np32
+from test_gpu_draft_rope import expect_append
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+# ----------------------------------------------------------------------------- numbers that are none
+
+@pytest.mark.parametrize("fmt", list(FORMATS))
+@pytest.mark.parametrize("dtype,rot,layout", [(torch.float32, 64, kvq.KVQ_ROPE_HALF), (torch.float16, 64, kvq.KVQ_ROPE_INTERLEAVED),
+                                              (torch.bfloat16, 24, kvq.KVQ_ROPE_HALF)])
+def test_nan_and_infinities_are_stored_as_kvq_append_stores_them(cuda_device, fmt, dtype, rot, layout):
+    B, n, hkv, dh, cap = 2, 9, 2, 64, 32
+    gen = torch.Generator().manual_seed(41)
+    cfg = make_cfg(fmt, B, cap, hkv, hkv, dh)
+    a, b = make_layer(cfg, gen), make_layer(cfg, gen)
+    k, v = (torch.randn(B, n, hkv, dh, generator=gen) * 2 for _ in range(2))
+    inf, nan = float("inf"), float("nan")
+    for x in (k, v):
+        x[0, 0, 0, 5] = nan
+        x[0, 1, :, 3], x[0, 1, 1, 40] = inf, nan
+        x[0, 2, 0, 60] = -inf
+        x[0, 3] = nan                                   # a row of nothing else
+        x[0, 4, 0, :32] = nan                           # a group of nothing else
+        x[0, 5, 1, 32:40], x[0, 5, 1, 7] = nan, -inf
+        x[0, 6, 0] = 0.0
+        x[0, 6, 0, 63] = nan                            # zeros beside it
+        x[1, 0, :, ::2] = nan
+    k, v = k.to(dtype).cuda(), v.to(dtype).cuda()
+    r = RopeConfig(rot, layout, base=500.0)
+    table = kvq.kvq_rope_table(r, cap)
+    pos = [0, 17]
+    kvq.kvq_rope_append(cfg, a, r, table, None, k, v, None, i32(pos), max(pos))
+    t = table.cpu().numpy()
+    with np.errstate(invalid="ignore"):
+        turned = np.stack([np.stack([rotated(to_np32(k[s, j]), t[pos[s] + j], rot, layout) for j in range(n)]) for s in range(B)])
+    kvq.kvq_append(cfg, b, torch.from_numpy(turned).cuda(), v.float(), i32(pos), max(pos), n)
+    for got, want, name in zip(logical(a, cfg), logical(b, cfg), ("k codes", "k scales", "v codes", "v scales")):
+        assert (got is None) == (want is None)
+        assert got is None or np.array_equal(got, want), (name, np.argwhere(got != want)[:8].tolist())
