@@ -477,7 +477,8 @@ KVQ_API int kvq_rope_table(const kvq_rope_config *rope, int32_t first_pos, int32
  * A token whose storage position is outside the cache (or whose page is invalid) is not
  * stored, but its query is rotated; a token whose rope position is outside the table is
  * skipped altogether.  Rows of tokens >= count_b are neither read nor written.
- * With a sliding window a token that a later one of the same call overwrites is not stored.
+ * With a sliding window a token that a later one of the same call overwrites is not stored
+ * (a skipped one overwrites nothing).
  * Errors: INVALID_ARG (h-mode included), UNSUPPORTED, CAPACITY (max_pos_host + n_new
  * beyond the capacity, or beyond table_len with d_rope_pos NULL), ALIGN, LAUNCH. */
 KVQ_API int kvq_rope_append(const kvq_config *cfg, const kvq_layer *layer,

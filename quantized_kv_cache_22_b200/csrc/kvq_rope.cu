@@ -323,8 +323,11 @@ __global__ void __launch_bounds__(32 * kRopeWarps, MODE == 2 ? 4 : 5)
     if (j >= count) return;
     const int first = p.d_pos[b];
     const int64_t pos = (int64_t)first + j;
-    const int64_t rp = p.d_rope_pos ? p.d_rope_pos[token] : pos;
-    if (rp < 0 || rp >= p.table_len) return;
+    // the rope position of the sequence's token at index `at`, and whether the table has it
+    auto rope_pos = [&](int64_t at) -> int64_t { return p.d_rope_pos ? p.d_rope_pos[(int64_t)b * p.n_new + at] : first + at; };
+    auto in_table = [&](int64_t rp) { return rp >= 0 && rp < p.table_len; };
+    const int64_t rp = rope_pos(j);
+    if (!in_table(rp)) return;
 
     const int sub = lane / LPR, t = lane % LPR;
     Turn<DH, MODE> turn;
@@ -361,10 +364,12 @@ __global__ void __launch_bounds__(32 * kRopeWarps, MODE == 2 ? 4 : 5)
         while (i - split >= nq) i -= split;      // (units past the last query's were skipped)
     }
     i -= nq;
-    // a token that a later token of this call overwrites in the ring is not stored
+    // a token that a later token of this call overwrites in the ring is not stored (one that is
+    // skipped overwrites nothing)
     bool keep = true;
     if (p.rows.window > 0 && pos >= p.rows.n_anchor)
-        keep = pos + p.rows.window > (int64_t)first + count - 1;
+#pragma unroll 1
+        for (int64_t at = (int64_t)j + p.rows.window; keep && at < count; at += p.rows.window) keep = !in_table(rope_pos(at));
     const int64_t row0 = keep ? cache_row(p.rows, b, 0, pos) : -1;       // head 0's row; heads lie apart by:
     const int64_t head_rows = p.rows.block_table ? kPageTokens : p.rows.cap;
     const int64_t from_k = row_of(p.k_in), from_v = row_of(p.v_in);

@@ -52,3 +52,33 @@ def test_nan_and_infinities_are_stored_as_kvq_append_stores_them(cuda_device, fm
     for got, want, name in zip(logical(a, cfg), logical(b, cfg), ("k codes", "k scales", "v codes", "v scales")):
         assert (got is None) == (want is None)
         assert got is None or np.array_equal(got, want), (name, np.argwhere(got != want)[:8].tolist())
+
+
+# ----------------------------------------------------------------------------- ring
+
+@pytest.mark.parametrize("n", [30, 56])
+def test_a_skipped_token_overwrites_nothing_in_the_ring(cuda_device, n):
+    """A token whose rope position is outside the table is skipped: the earlier token of the call that
+    shares its slot stays."""
+    gen = torch.Generator().manual_seed(42)
+    B, window, anchor = 3, 24, 8
+    cfg = make_cfg("k8v4g32", B, 32, 2, 1, 128, window=window, n_anchor=anchor)
+    layer = make_layer(cfg, gen)
+    r = RopeConfig(64)
+    table = kvq.kvq_rope_table(r, 200)
+    k, v = (torch.randn(B, n, 1, 128, generator=gen).half().cuda() for _ in range(2))
+    pos = [4, 77, 0]
+    rope_pos = [[p + j for j in range(n)] for p in pos]
+    for j in (24, 27, 28, n - 1):
+        rope_pos[0][j] = 200
+    for j in range(26, n, 3):
+        rope_pos[1][j] = -1
+    for j in range(24, n):
+        rope_pos[2][j] = 2**31 - 1
+    count = [n, n, n - 2]
+    before = logical(layer, cfg)
+    kvq.kvq_rope_append(cfg, layer, r, table, None, k, v, None, i32(pos), 100, d_count=i32(count), d_rope_pos=i32(rope_pos))
+    torch.cuda.synchronize()
+    _, want = expect_append(cfg, before, None, k, v, table.cpu().numpy(), 64, kvq.KVQ_ROPE_HALF, pos, count, rope_pos)
+    for g, w in zip(logical(layer, cfg), want):
+        assert np.array_equal(g, w)
