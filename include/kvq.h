@@ -548,7 +548,8 @@ KVQ_API int kvq_tree_attn(const kvq_config *cfg, const kvq_layer *layer, const v
  * indices in strictly ascending order below n_tree (a path from the root of a tree whose
  * parents precede their children); m is d_n_path[b] clamped to [0, path_stride], cut before
  * the first index that breaks this.  Other rows stay as they were.
- *   layers   host array of n_layers layers of this config, none twice (one launch per 64)
+ *   layers   host array of n_layers layers of this config, none twice (one launch per 64); they
+ *            may share one page pool, each with a block table and pages of its own
  *   d_len_out  device int32 [B] or NULL: receives L + m; not d_len itself
  *   max_len_host  host bound of d_len[]: max_len_host + n_tree <= capacity
  *   path_stride  1 .. n_tree;  n_tree  1 .. KVQ_TREE_MAX

@@ -308,12 +308,19 @@ int kvq_tree_commit(const kvq_config *cfg, const kvq_layer *layers, int32_t n_la
         return KVQ_ERR_INVALID_ARG;
     if (cfg->window != 0) return KVQ_ERR_UNSUPPORTED;
     if ((int64_t)max_len_host + n_tree > cfg->capacity) return KVQ_ERR_CAPACITY;
+    // Two layers of the same rows: two warps' moves would race.  Layers may have one page pool, with a
+    // block table each.
+    const bool ks = scale_row_vals(cfg, cfg->k_bits, cfg->k_group) != 0, vs = scale_row_vals(cfg, cfg->v_bits, cfg->v_group) != 0;
+    auto same_rows = [&](const kvq_layer &a, const kvq_layer &b) {
+        if (cfg->page_tokens && a.block_table != b.block_table) return false;
+        return a.k_codes == b.k_codes || a.v_codes == b.v_codes || (ks && a.k_scales == b.k_scales) ||
+               (vs && a.v_scales == b.v_scales);
+    };
     for (int32_t i = 0; i < n_layers; i++) {
         rc = check_kv_layer(cfg, &layers[i]);
         if (rc) return rc;
-        // (moves of the same rows by two warps would race)
         for (int32_t j = 0; j < i; j++)
-            if (layers[j].k_codes == layers[i].k_codes || layers[j].v_codes == layers[i].v_codes) return KVQ_ERR_INVALID_ARG;
+            if (same_rows(layers[j], layers[i])) return KVQ_ERR_INVALID_ARG;
     }
     CommitParams p{};
     p.rows = cache_rows(cfg, nullptr);

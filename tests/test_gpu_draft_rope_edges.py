@@ -82,3 +82,36 @@ def test_a_skipped_token_overwrites_nothing_in_the_ring(cuda_device, n):
     _, want = expect_append(cfg, before, None, k, v, table.cpu().numpy(), 64, kvq.KVQ_ROPE_HALF, pos, count, rope_pos)
     for g, w in zip(logical(layer, cfg), want):
         assert np.array_equal(g, w)
+
+
+# ----------------------------------------------------------------------------- commit
+
+@pytest.mark.parametrize("fmt,dh", [("k8v8", 128), ("k4v4g32", 64), ("tensor", 128)])
+def test_commit_in_layers_that_share_a_page_pool(cuda_device, fmt, dh):
+    """One pool of pages for all layers, a block table each."""
+    B, hkv, cap, T, n_layers = 2, 2, 256, 9, 3
+    gen = torch.Generator().manual_seed(43)
+    cfg = make_cfg(fmt, B, cap, hkv, hkv, dh, n_pages=2 * B * n_layers + 1)
+    pool = make_layer(cfg, gen)
+    for x in (pool.k_codes, pool.v_codes):
+        x.random_(0, 256)
+    if fmt != "tensor":
+        pool.k_scales.uniform_(0, 1)
+        pool.v_scales.uniform_(0, 1)
+    pages = torch.randperm(cfg.n_pages, generator=gen)[: 2 * B * n_layers].view(n_layers, B, 2).to(torch.int32).cuda()
+    layers = [LayerCache.from_buffers(cfg, pool.k_codes, pool.k_scales, pool.v_codes, pool.v_scales, block_table=pages[i])
+              for i in range(n_layers)]
+    before = [logical(x, cfg) for x in layers]
+    lens, path = [120, 200], [1, 4, 8]
+    new = i32([0, 0])
+    kvq.kvq_tree_commit(cfg, layers, i32(lens), 200, i32([path] * B), i32([3, 2]), T, d_len_out=new)
+    assert new.tolist() == [123, 202]
+    for layer, was in zip(layers, before):
+        for g, w in zip(logical(layer, cfg), was):
+            if w is None:
+                continue
+            want = w.copy()
+            for b, m in enumerate((3, 2)):
+                for i in range(m):
+                    want[b, :, lens[b] + i] = w[b, :, lens[b] + path[i]]
+            assert np.array_equal(g, want)
