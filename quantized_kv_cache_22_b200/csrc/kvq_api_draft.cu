@@ -83,8 +83,9 @@ void rope_frequencies(const kvq_rope_config *r, double *freq, double *gain)
         // the pair that turns n times in orig_len: orig_len base^(-2i / rot) / 2 pi = n
         lo = std::floor(rot * std::log(r->orig_len / (r->high * two_pi)) / (2.0 * std::log(base)));
         hi = std::ceil(rot * std::log(r->orig_len / (r->low * two_pi)) / (2.0 * std::log(base)));
-        lo = std::max(lo, 0.0);
-        hi = std::min(hi, (double)(rot - 1));
+        // (where even pair 0 turns less than `low` times, the ramp ends before it)
+        lo = hi < 0.0 ? -1.0 : std::max(lo, 0.0);
+        hi = hi < 0.0 ? 0.0 : std::min(hi, (double)(rot - 1));
     }
     for (int i = 0; i < pairs; i++) {
         const double f = std::pow(base, -2.0 * i / rot);

@@ -84,6 +84,19 @@ def test_a_skipped_token_overwrites_nothing_in_the_ring(cuda_device, n):
         assert np.array_equal(g, w)
 
 
+# ----------------------------------------------------------------------------- table
+
+@pytest.mark.parametrize("orig_len,low,high", [(4, 1.0, 32.0), (1, 1.0, 2.0), (2048, 1000.0, 2000.0)])
+def test_yarn_where_every_pair_turns_less_than_low(cuda_device, orig_len, low, high):
+    r = RopeConfig(64, scaling=kvq.KVQ_ROPE_YARN, factor=8.0, orig_len=orig_len, low=low, high=high, gain=1.0)
+    assert orig_len / (2 * math.pi) < low                     # pair 0 turns the most
+    angle = np.arange(40, dtype=np.float64)[:, None] * (10000.0 ** (-2 * np.arange(32) / 64) / 8)
+    want = np.stack([np.cos(angle), np.sin(angle)], -1)
+    got = kvq.kvq_rope_table(r, 40).cpu().numpy()
+    # half an fp32 step, and the roundings of the angle in 64 bits
+    assert np.all(np.abs(got - want) <= 2.0 ** -24 * np.abs(want) + (angle[..., None] + 1) * 2.0 ** -50)
+
+
 # ----------------------------------------------------------------------------- commit
 
 @pytest.mark.parametrize("fmt,dh", [("k8v8", 128), ("k4v4g32", 64), ("tensor", 128)])
