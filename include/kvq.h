@@ -587,6 +587,20 @@ KVQ_API int kvq_selftest_decode_timeout(const kvq_config *cfg, const kvq_layer *
                                         uint64_t workspace_bytes, uint64_t timeout_ns,
                                         kvq_stream_t stream);
 
+/* The same for kvq_tree_attn (causal mask, every token drafted): the wait limit is
+ * timeout_ns (1 ns .. 2 s), and a CTA's producer copies the tiles of its first
+ * n_segments segments only (a segment: the CTA's run of tiles of one sequence, KV head
+ * and tile of query rows).  The waits of a CTA with more run out, KVQ_ERR_TIMEOUT is
+ * recorded and `out` is unspecified; the workspace is ready for its next use.  Other
+ * arguments and errors as kvq_tree_attn. */
+KVQ_API int kvq_selftest_tree_timeout(const kvq_config *cfg, const kvq_layer *layer,
+                                      const void *q, int32_t q_dtype, int32_t n_tree,
+                                      const int32_t *d_len, int32_t max_len_host, void *out,
+                                      int32_t out_dtype, void *workspace,
+                                      uint64_t workspace_bytes, int32_t num_ctas,
+                                      int32_t n_segments, uint64_t timeout_ns,
+                                      kvq_stream_t stream);
+
 /* Bytes of the device array behind kvq_decode_attn_noalloc (8 MiB). */
 #define KVQ_NOALLOC_SCRATCH_BYTES (8u * 1024u * 1024u)
 

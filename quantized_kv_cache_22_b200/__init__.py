@@ -34,7 +34,7 @@ EXPORTED = ("kvq_cache_bytes", "kvq_layer_buffer_bytes", "kvq_append", "kvq_work
             "kvq_h_fused_scratch_bytes", "kvq_h_decode_fused", "kvq_selftest_bounded_wait",
             "kvq_selftest_decode_timeout", "kvq_noalloc_status", "kvq_selftest_noalloc_timeout",
             "kvq_decode_plan_info", "kvq_rope_table", "kvq_rope_append", "kvq_read",
-            "kvq_tree_workspace_bytes", "kvq_tree_attn", "kvq_tree_commit")
+            "kvq_tree_workspace_bytes", "kvq_tree_attn", "kvq_tree_commit", "kvq_selftest_tree_timeout")
 
 
 class KvqError(RuntimeError):
@@ -121,6 +121,7 @@ def _load():
         "kvq_tree_attn": [cfgp, layp, P, i32, i32, P, i32, P, P, ctypes.c_float, P, i32, P, u64,
                           i32, P],
         "kvq_tree_commit": [cfgp, P, i32, P, i32, i32, P, i32, P, P, P],
+        "kvq_selftest_tree_timeout": [cfgp, layp, P, i32, i32, P, i32, P, i32, P, u64, i32, i32, u64, P],
     })
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -675,3 +676,16 @@ def kvq_tree_commit(cfg: Config, layers, d_len: torch.Tensor, max_len: int, d_pa
     _check("kvq_tree_commit", _lib.kvq_tree_commit(
         cfg._ref(), b"".join([x._kept()[1] for x in layers]), len(layers), _ptr(d_len), int(max_len), int(n_tree), _ptr(d_path), d_path.shape[1],
         _ptr(d_n_path), _ptr(d_len_out), st))
+
+
+def kvq_selftest_tree_timeout(cfg: Config, layer: LayerCache, q: torch.Tensor, d_len: torch.Tensor, max_len: int,
+                              out: torch.Tensor, ws: TreeWorkspace, n_segments: int, timeout_ns: int,
+                              num_ctas: int = 0, stream=None):
+    """kvq_tree_attn with a producer that stops after n_segments segments: its waits run out (see kvq.h)."""
+    _need(q.dim() == 4 and q.shape == out.shape == (cfg.batch, q.shape[1], cfg.n_q_heads, cfg.head_dim)
+          and q.is_contiguous() and out.is_contiguous(), "q and out are contiguous [B][n_tree][Hq][Dh]")
+    st = _here(stream, (layer,), q, d_len, out, ws.buf)
+    _ints(d_len, (cfg.batch,), "d_len")
+    _check("kvq_selftest_tree_timeout", _lib.kvq_selftest_tree_timeout(
+        cfg._ref(), layer._ref(), _ptr(q), _dtype_code(q), q.shape[1], _ptr(d_len), int(max_len), _ptr(out),
+        _dtype_code(out), _ptr(ws.buf), ws.nbytes, int(num_ctas), int(n_segments), int(timeout_ns), st))

@@ -127,6 +127,60 @@ int check_draft(const kvq_config *cfg, const kvq_layer *layer)
     return check_kv_layer(cfg, layer);
 }
 
+// kvq_tree_attn with its wait limit, and the segments that each CTA's producer copies.
+int tree_attn(const kvq_config *cfg, const kvq_layer *layer, const void *q, int32_t q_dtype, int32_t n_tree,
+              const int32_t *d_len, int32_t max_len_host, const int32_t *d_n_tree, const uint64_t *d_mask,
+              float softmax_scale, void *out, int32_t out_dtype, void *workspace, uint64_t workspace_bytes,
+              int32_t num_ctas, uint64_t timeout_ns, int32_t serve, kvq_stream_t stream)
+{
+    int rc = check_draft(cfg, layer);
+    if (rc) return rc;
+    if (!q || !d_len || !out || !workspace || num_ctas < 0 || max_len_host < 0 || n_tree < 1 ||
+        n_tree > KVQ_TREE_MAX || !valid_dtype(q_dtype) || !valid_dtype(out_dtype) || !std::isfinite(softmax_scale))
+        return KVQ_ERR_INVALID_ARG;
+    if ((int64_t)max_len_host + n_tree > cfg->capacity) return KVQ_ERR_CAPACITY;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || (reinterpret_cast<uintptr_t>(d_mask) & 7u))
+        return KVQ_ERR_ALIGN;
+    uint64_t need = 0;
+    rc = kvq_tree_workspace_bytes(cfg, n_tree, num_ctas, &need);
+    if (rc) return rc;
+    if (workspace_bytes < need) return KVQ_ERR_WORKSPACE;
+    TreeParams p{};
+    p.rows = cache_rows(cfg, layer->block_table);
+    p.k = cache_tensor(layer->k_codes, layer->k_scales, cfg->k_bits, cfg->k_group);
+    p.v = cache_tensor(layer->v_codes, layer->v_scales, cfg->v_bits, cfg->v_group);
+    p.q = q;
+    p.out = out;
+    p.d_len = d_len;
+    p.d_n_tree = d_n_tree;
+    p.d_mask = d_mask;
+    p.q_dtype = q_dtype;
+    p.out_dtype = out_dtype;
+    p.fmt = cfg->kv_format;
+    p.n_tree = n_tree;
+    p.n_q_heads = cfg->n_q_heads;
+    p.G = cfg->n_q_heads / cfg->n_kv_heads;
+    p.dh = cfg->head_dim;
+    const float scale = softmax_scale != 0.f ? softmax_scale : 1.f / std::sqrt((float)cfg->head_dim);
+    p.tau_log2e = scale * 1.4426950408889634f;
+    p.timeout_ns = timeout_ns;
+    p.serve = serve;
+    p.row_tiles = tree_row_tiles(n_tree, p.G);
+    p.slot_rows = tree_slot_rows(n_tree, p.G);
+    p.status = static_cast<int *>(workspace);
+    uint8_t *ws = static_cast<uint8_t *>(workspace) + kWorkspaceHeaderFloats * 4;
+    p.seg = reinterpret_cast<int4 *>(ws);
+    p.slots = reinterpret_cast<float *>(ws + tree_seg_bytes(cfg, n_tree, p.G));
+    int sms = 0, max_smem = 0;
+    rc = current_device_props(&sms, &max_smem);
+    if (rc) return rc;
+    if (!plan_tree(p, max_smem, &p.l)) return KVQ_ERR_UNSUPPORTED;
+    rc = tree_ctas(num_ctas, &p.l.num_ctas);
+    if (rc) return rc;
+    cudaError_t e = launch_tree(p, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? KVQ_OK : fail("tree attention launch", e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -251,51 +305,18 @@ int kvq_tree_attn(const kvq_config *cfg, const kvq_layer *layer, const void *q, 
                   float softmax_scale, void *out, int32_t out_dtype, void *workspace, uint64_t workspace_bytes,
                   int32_t num_ctas, kvq_stream_t stream)
 {
-    int rc = check_draft(cfg, layer);
-    if (rc) return rc;
-    if (!q || !d_len || !out || !workspace || num_ctas < 0 || max_len_host < 0 || n_tree < 1 ||
-        n_tree > KVQ_TREE_MAX || !valid_dtype(q_dtype) || !valid_dtype(out_dtype) || !std::isfinite(softmax_scale))
-        return KVQ_ERR_INVALID_ARG;
-    if ((int64_t)max_len_host + n_tree > cfg->capacity) return KVQ_ERR_CAPACITY;
-    if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || (reinterpret_cast<uintptr_t>(d_mask) & 7u))
-        return KVQ_ERR_ALIGN;
-    uint64_t need = 0;
-    rc = kvq_tree_workspace_bytes(cfg, n_tree, num_ctas, &need);
-    if (rc) return rc;
-    if (workspace_bytes < need) return KVQ_ERR_WORKSPACE;
-    TreeParams p{};
-    p.rows = cache_rows(cfg, layer->block_table);
-    p.k = cache_tensor(layer->k_codes, layer->k_scales, cfg->k_bits, cfg->k_group);
-    p.v = cache_tensor(layer->v_codes, layer->v_scales, cfg->v_bits, cfg->v_group);
-    p.q = q;
-    p.out = out;
-    p.d_len = d_len;
-    p.d_n_tree = d_n_tree;
-    p.d_mask = d_mask;
-    p.q_dtype = q_dtype;
-    p.out_dtype = out_dtype;
-    p.fmt = cfg->kv_format;
-    p.n_tree = n_tree;
-    p.n_q_heads = cfg->n_q_heads;
-    p.G = cfg->n_q_heads / cfg->n_kv_heads;
-    p.dh = cfg->head_dim;
-    const float scale = softmax_scale != 0.f ? softmax_scale : 1.f / std::sqrt((float)cfg->head_dim);
-    p.tau_log2e = scale * 1.4426950408889634f;
-    p.timeout_ns = kTimeoutNs;
-    p.row_tiles = tree_row_tiles(n_tree, p.G);
-    p.slot_rows = tree_slot_rows(n_tree, p.G);
-    p.status = static_cast<int *>(workspace);
-    uint8_t *ws = static_cast<uint8_t *>(workspace) + kWorkspaceHeaderFloats * 4;
-    p.seg = reinterpret_cast<int4 *>(ws);
-    p.slots = reinterpret_cast<float *>(ws + tree_seg_bytes(cfg, n_tree, p.G));
-    int sms = 0, max_smem = 0;
-    rc = current_device_props(&sms, &max_smem);
-    if (rc) return rc;
-    if (!plan_tree(p, max_smem, &p.l)) return KVQ_ERR_UNSUPPORTED;
-    rc = tree_ctas(num_ctas, &p.l.num_ctas);
-    if (rc) return rc;
-    cudaError_t e = launch_tree(p, reinterpret_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? KVQ_OK : fail("tree attention launch", e);
+    return tree_attn(cfg, layer, q, q_dtype, n_tree, d_len, max_len_host, d_n_tree, d_mask, softmax_scale, out, out_dtype,
+                     workspace, workspace_bytes, num_ctas, kTimeoutNs, INT32_MAX, stream);
+}
+
+int kvq_selftest_tree_timeout(const kvq_config *cfg, const kvq_layer *layer, const void *q, int32_t q_dtype,
+                              int32_t n_tree, const int32_t *d_len, int32_t max_len_host, void *out, int32_t out_dtype,
+                              void *workspace, uint64_t workspace_bytes, int32_t num_ctas, int32_t n_segments,
+                              uint64_t timeout_ns, kvq_stream_t stream)
+{
+    if (n_segments < 0 || timeout_ns == 0 || timeout_ns > 2000000000ull) return KVQ_ERR_INVALID_ARG;
+    return tree_attn(cfg, layer, q, q_dtype, n_tree, d_len, max_len_host, nullptr, nullptr, 0.f, out, out_dtype, workspace,
+                     workspace_bytes, num_ctas, timeout_ns, n_segments, stream);
 }
 
 int kvq_tree_commit(const kvq_config *cfg, const kvq_layer *layers, int32_t n_layers, const int32_t *d_len,

@@ -167,6 +167,8 @@ struct TreeParams {
     int32_t n_tree, n_q_heads, G, dh;
     int32_t row_tiles, slot_rows;     // tiles of kTreeRows query rows of a KV head, rows of a slot
     float tau_log2e;
+    int32_t serve;                    // segments whose tiles a CTA's producer copies: all of them but
+                                      // in kvq_selftest_tree_timeout
     uint64_t timeout_ns;
     TreeLaunch l;
 };

@@ -1055,9 +1055,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             const int vsb = sc && p.v.bits != 16 ? DH / p.v.group * scale_vals(p.fmt) * 2 : 0;
             int e = 0, s = 0, use = 0;          // entries filled; the next one's place and use
             bool ok = true;
+            int serve = p.serve;                // segments to copy (self-test: the rest is withheld)
             Walk it;
 #pragma unroll 1
             for (it.start(p, w); it.count && ok; it.next(p)) {
+                if (serve-- <= 0) break;
 #pragma unroll 1
                 for (int t = it.tile; t < it.tile + it.count && ok; t++) {
                     const int nv = min(TT, it.s.total - t * TT);
