@@ -522,8 +522,9 @@ KVQ_API int kvq_read(const kvq_config *cfg, const kvq_layer *layer, const kvq_ro
  * enter the second product as p_t * (value scale) rounded to fp16: each is off by 2^-11 of
  * itself, or by 2^-30 of the row's largest p_t * scale where that is more.  A token whose
  * value scale is zero (its codes are zeros, as every append writes them) counts in the sum of
- * the probabilities only.  A row that attends nothing gets zeros; rows i >= n are left as
- * they were.
+ * the probabilities only.  A value row's one scale is not negative (no append writes such; a
+ * tensor's scale may be).  A row that attends nothing gets zeros; rows i >= n are left as they
+ * were.
  * Masked places do not reach a row, whatever they hold; a row that attends a non-finite
  * key or value gets an unspecified result.
  *   q        device [B][n_tree][Hq][Dh], q_dtype KVQ_F16, KVQ_F32 or KVQ_BF16; G <= 8

@@ -17,7 +17,7 @@ namespace {
 // of kReadUnroll rows at a time, all their loads in flight first, and in a cache that is
 // neither paged nor a ring (FLAT) addresses advance by constants.  A block takes consecutive
 // tokens of one head of K or of V.
-// 16 x 8192 tokens of 8 heads of 128, INT8 to f16: 139 to 145 us, 5.6 to 5.8 TB/s, 85 to 89% of
+// 16 x 8192 tokens of 8 heads of 128, INT8 to f16: 139 to 146 us, 5.5 to 5.8 TB/s, 85 to 89% of
 // what a copy reaches (two rows in flight: 150; the addresses of a paged cache: 149 against 145
 // in the same run; one piece a lane: 174, three quarters of the issue slots taken).
 // Every code is exact in f16.  For F16 outputs the product with the scale is taken in f16:

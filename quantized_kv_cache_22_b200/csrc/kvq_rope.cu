@@ -216,9 +216,9 @@ struct Raw16 {
 // registers and walk the token's query, key and value rows.  `split` warps share a token so
 // that a decode step's few tokens still fill the GPU.
 // HBM bounds it in theory, latency and instructions in practice: 2 x 4096 tokens of 32 query
-// and 8 KV heads of 128, bf16 in, INT8 in the cache: 41 us, 4.5 TB/s (with eight elements a
+// and 8 KV heads of 128, bf16 in, INT8 in the cache: 41.7 us, 4.4 TB/s (with eight elements a
 // lane, run-time types and divisions by the group size it took 7200 instructions a token and
-// three times as long); a step of 64 tokens 3.9 us.
+// three times as long); a step of 64 tokens 3.2 us.
 // MODE 0: half layout, whole row; 1: interleaved; 2: half layout, part of the row (partners
 // are read a second time, from the cache line that a neighbour has just fetched).
 template <int DH, int MODE>

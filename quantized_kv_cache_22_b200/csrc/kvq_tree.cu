@@ -40,9 +40,9 @@
 //     that all four warps share the exponentials; the copies' sums are joined at the end.
 //     (64 rows: 119 us against 145 without copies; 32 rows: 160 against 266.)
 //
-// What bounds it.  16 x 8192 tokens of 8 KV heads, INT8, 4 heads a group: 118 us with 16 drafted
-// tokens (64 rows a KV head; its bytes alone would take 42), 285 with 64 (two row tiles, every
-// tile converted for both; the products alone 84).  With 16, a tile of 128 tokens takes 3400
+// What bounds it.  16 x 8192 tokens of 8 KV heads, INT8, 4 heads a group: 114 to 121 us with 16
+// drafted tokens (64 rows a KV head; its bytes alone would take 42), 276 to 292 with 64 (two row
+// tiles, every tile converted for both; the products alone 84).  With 16, a tile of 128 tokens takes 3400
 // cycles, of which the tensor cores work 1000 and the issue slots 1500 (conversion of 32
 // thousand codes, 8 thousand exponentials); the rest is the chain scores - softmax - product of
 // a tile, through three barriers of 100 cycles and more each.  Steps that measured well: K and V
@@ -50,8 +50,11 @@
 // its own and whole query rows in one load, 130 -> 125; a tile's scores in one product instead of
 // two, 125 -> 113.  Groups that take tiles in turns instead of halves of each made short segments
 // 5% faster.  A segment pays the opening of its row tile and its output, 8 to 12 thousand cycles
-// with code and constants fetched cold: 64 sequences of 4000 tokens, INT4 in pages, 8 drafted,
-// 160 us; 8 ragged ones of up to 2011, K INT8 and V INT4 in groups of 32, 24 drafted, 49 us.
+// with code and constants fetched cold, as much as three tiles, which the split over the CTAs does
+// not count: of 64 sequences of up to 4000 tokens, INT4 in pages, 8 drafted, a CTA has 4.4 segments
+// on average and 12 at most, 162 us; of 8 ragged ones of up to 2011, K INT8 and V INT4 in groups of
+// 32, 24 drafted, 1.3 and 4, 49 us.  ptxas spills 716 bytes (880 with Dh 64) at the 96 registers that
+// 640 threads leave.  Code of the same work moves the 64 sequences' time by 1 to 3%.
 //
 // Every wait is bounded; a give-up records KVQ_ERR_TIMEOUT in the workspace's status word.
 #include <algorithm>
